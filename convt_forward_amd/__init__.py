@@ -504,3 +504,17 @@ def conv_transpose_backward_data(dy, w, x_shape, stride=1, padding=0, dilation=1
                   padding, dilation, output_padding, groups, False, torch_dtype_name(dy), "auto",
                   route, filter_layout, taps_flipped)
     return pl.backward_data(dy, w, dx=dx, workspace=workspace, stream=stream)
+
+
+# The decoding-step operators need torch at import; the rest of this module
+# does not, so they are loaded on first use.
+_DECODE = ("ATTEND_ROUTES", "KVCache", "Q4_ROUTES", "attend_plan", "cache_read", "cache_slots", "cache_write",
+           "decode_attention", "q4_matvec", "q4_quantise", "rms_norm")
+
+
+def __getattr__(name):
+    if name in _DECODE:
+        from . import decode
+        value = globals()[name] = getattr(decode, name)
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,604 @@
+"""GPU tests of the decoding-step operators against their plain 64-bit forms (tests/decode_util.py
+derives the bounds): sizes that end inside a piece, a tile or a page, strides, empty rows,
+NaN and infinities in places that must not be read, pages outside the cache, offsets past 32
+bits, other streams and graph replays."""
+import math
+
+import pytest
+import torch
+
+import convt_forward_amd as C
+from tests.decode_util import (E4M3, TYPES, U, attend64, attend_bound, norm64, quantised_bound, rounding, within)
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+def rand(*shape, seed=0, scale=1.0):
+    g = torch.Generator().manual_seed(seed + 1000 * len(shape) + sum(shape))
+    return torch.randn(*shape, generator=g) * scale
+
+
+# ---------------------------------------------------------------- rms_norm
+
+
+def check_norm(x, w, res, eps, quantise, dt, **kw):
+    """x, w, res on the host in the element type."""
+    y, scale, h = C.rms_norm(x.to(DEV), w.to(DEV), residual=None if res is None else res.to(DEV), eps=eps,
+                             quantise=quantise, **kw)
+    torch.cuda.synchronize()
+    want, want_h = norm64(x, w, res, eps)
+    # the sum of squares: at most width / 1024 + 64 roundings on the way of any term
+    rel = (x.shape[-1] / 1024 + 64 + 8) * U
+    if res is not None:
+        # h itself is one float32 sum, then one rounding
+        within(h, want_h, rounding(TYPES[dt], want_h) + want_h.abs() * 2 * U, "residual")
+    else:
+        assert h is None
+    if not quantise:
+        assert scale is None
+        within(y, want, rounding(TYPES[dt], want) + want.abs() * rel, "norm")
+        return
+    assert y.dtype == E4M3 and scale.shape == x.shape[:-1]
+    s64 = (want.abs().amax(-1) / 448).clamp(min=2.0 ** -126)
+    within(scale, s64, s64 * (rel + 2 * U), "scale")
+    within(y.double() * scale.double().unsqueeze(-1), want, quantised_bound(want, s64) + want.abs() * 2 * rel, "codes")
+
+
+@pytest.mark.parametrize("dt", sorted(TYPES))
+@pytest.mark.parametrize("quantise", [False, True])
+@pytest.mark.parametrize("width", [1, 7, 8, 64, 511, 512, 1000, 1024, 1025, 2048, 4095, 5001, 8192, 16384, 16400, 32768, 40003])
+def test_norm_widths(dt, quantise, width):
+    print(f"norm {dt} width {width} quantise {quantise}", flush=True)
+    rows = 5 if width < 9000 else 2
+    t = TYPES[dt]
+    x, res = rand(rows, width).to(t), rand(rows, width, seed=1, scale=4).to(t)
+    w = (1 + rand(width, seed=2, scale=0.2)).to(t)
+    check_norm(x, w, res, 1e-6, quantise, dt)
+    check_norm(x, w, None, 1e-5, quantise, dt)
+
+
+@pytest.mark.parametrize("rows", [0, 1, 3, 4, 5, 257, 4100])
+@pytest.mark.parametrize("quantise", [False, True])
+def test_norm_rows(rows, quantise):
+    check_norm(rand(rows, 96).bfloat16(), torch.ones(96).bfloat16(), rand(rows, 96, seed=3).bfloat16(), 1e-6, quantise, "bf16")
+
+
+@pytest.mark.parametrize("quantise", [False, True])
+def test_norm_strides_axes_and_in_place(quantise):
+    # odd row spacing, so that rows start at any two-byte address
+    big = rand(6, 203).half()
+    x, w = big[:, 3:100], torch.ones(97).half()
+    res = rand(6, 97, seed=4).half()
+    xd, rd = big.to(DEV)[:, 3:100], res.to(DEV)
+    y, s, h = C.rms_norm(xd, w.to(DEV), residual=rd, residual_out=rd, quantise=quantise)
+    assert h is rd
+    y2, s2, h2 = C.rms_norm(x.contiguous().to(DEV), w.to(DEV), residual=res.to(DEV), quantise=quantise)
+    assert torch.equal(h, h2) and torch.equal(y.float(), y2.float()) and (not quantise or torch.equal(s, s2))
+    # leading axes, a given output with its own spacing
+    x3 = rand(2, 3, 97, seed=5).half()
+    out = torch.full((2, 3, 120), float("nan"), device=DEV).to(E4M3 if quantise else torch.float16)
+    y3, s3, _ = C.rms_norm(x3.to(DEV), w.to(DEV), quantise=quantise, y=out[:, :, 10:107])
+    y4, s4, _ = C.rms_norm(x3.reshape(6, 97).to(DEV), w.to(DEV), quantise=quantise)
+    assert torch.equal(y3.float().reshape(6, 97), y4.float())
+    assert out[:, :, :10].float().isnan().all() and out[:, :, 107:].float().isnan().all()
+    if quantise:
+        assert s3.shape == (2, 3) and torch.equal(s3.reshape(6), s4)
+    else:
+        xi = x3.to(DEV)
+        C.rms_norm(xi, w.to(DEV), y=xi)
+        assert torch.equal(xi.reshape(6, 97), y4)
+
+
+@pytest.mark.parametrize("width", [40, 3000, 40000])
+def test_norm_special_values(width):
+    x = rand(6, width)
+    x[0] = 0
+    x[1, width // 2] = math.nan
+    x[2, 1] = math.inf
+    x[3] *= 1e-30
+    x[4] *= 1e15
+    w = torch.ones(width)
+    y, s, _ = C.rms_norm(x.to(DEV), w.to(DEV), eps=1e-6, quantise=True)
+    back = (y.float() * s.unsqueeze(-1)).cpu()
+    assert (back[0] == 0).all() and s[0].item() == 2.0 ** -126
+    assert back[1].isnan().all() and back[2].isnan().all()
+    assert back[[3, 4, 5]].isfinite().all()
+    y, _, _ = C.rms_norm(x.to(DEV), w.to(DEV), eps=1e-6)
+    assert (y[0] == 0).all() and y[1].isnan().all() and y[2, 1].isnan().item() and (y[2, 2:] == 0).all()
+    check_norm(x[3:], w, None, 1e-6, False, "f32")
+
+
+def test_norm_refuses():
+    x, w = torch.zeros(2, 8, device=DEV), torch.ones(8, device=DEV)
+    for kw in [dict(residual=torch.zeros(2, 7, device=DEV)), dict(residual=x.half()), dict(residual_out=x),
+               dict(scale=torch.zeros(2, device=DEV)), dict(y=x.half()), dict(residual=torch.zeros(2, 8))]:
+        with pytest.raises(ValueError):
+            C.rms_norm(x, w, **kw)
+    with pytest.raises(ValueError):
+        C.rms_norm(x, torch.ones(9, device=DEV))
+    with pytest.raises(C.ConvtError):
+        C.rms_norm(x, w, eps=-1.0)
+    with pytest.raises(C.ConvtError):
+        C.rms_norm(x[:, :0], w[:0])
+
+
+# ---------------------------------------------------------------- cache
+
+
+def new_cache(pages, heads, page, dim, t, quantised, token_major=False, fill=None):
+    """A cache whose places hold `fill` (NaN by default): what is not written must not be read."""
+    kind = E4M3 if quantised else t
+    shape = (pages, page, heads, dim) if token_major else (pages, heads, page, dim)
+    k, v = (torch.full(shape, math.nan if fill is None else fill, device=DEV).to(kind) for _ in range(2))
+    if token_major:
+        k, v = k.transpose(1, 2), v.transpose(1, 2)
+    sc = [torch.full((pages, heads, page), math.nan if fill is None else fill, device=DEV) for _ in range(2)] if quantised else [None, None]
+    return C.KVCache(k, v, *sc)
+
+
+def plain_rows(x, quantised):
+    """The rows (float64) that a cache gives back for x, from the format's definition in float32."""
+    if not quantised:
+        return x.double()
+    s = (x.float().abs().amax(-1) / 448).clamp(min=2.0 ** -126)
+    q = (x.float() * (1 / s).unsqueeze(-1)).to(E4M3)
+    return q.double() * s.double().unsqueeze(-1)
+
+
+@pytest.mark.parametrize("dt", sorted(TYPES))
+@pytest.mark.parametrize("quantised", [False, True])
+@pytest.mark.parametrize("dim", [1, 5, 8, 64, 80, 128, 200, 512])
+def test_cache_write_and_read(dt, quantised, dim):
+    print(f"cache {dt} quantised {quantised} dim {dim}", flush=True)
+    t = TYPES[dt]
+    heads, page, pages, tokens = 3, 5, 9, 29
+    cache = new_cache(pages, heads, page, dim, t, quantised, token_major=dim in (5, 128))
+    k, v = rand(tokens, heads, dim).to(t), rand(tokens, heads, dim, seed=1, scale=1e-3).to(t)
+    k[3, 1] = 0
+    slots = torch.randperm(pages * page, generator=torch.Generator().manual_seed(dim))[:tokens]
+    slots[[2, 11, 20]] = torch.tensor([-1, pages * page, 2 ** 40])
+    C.cache_write(cache, k.to(DEV), v.to(DEV), slots.to(DEV))
+    kk, vv = C.cache_read(cache, slots.to(DEV), dtype=t)
+    torch.cuda.synchronize()
+    inside = (slots >= 0) & (slots < pages * page)
+    for got, x, name in ((kk, k, "k"), (vv, v, "v")):
+        back = got.cpu()
+        assert (back[~inside] == 0).all()
+        want = plain_rows(x, quantised)
+        if quantised:
+            # the codes are the format's; against the row itself, half a step of the format
+            within(back[inside], want[inside], rounding(t, want[inside]) + want[inside].abs() * 2 * U, name)
+            s = (x.double().abs().amax(-1) / 448).clamp(min=2.0 ** -126)
+            within(back[inside], x.double()[inside], (quantised_bound(x.double(), s) + rounding(t, x.double()) * (1 + 2.0 ** -3))[inside], name + " row")
+        else:
+            assert torch.equal(back[inside], x[inside])
+    # places that no slot named keep what they held
+    used = torch.zeros(pages * page, dtype=torch.bool)
+    used[slots[inside]] = True
+    kept = cache.k.float().cpu().transpose(1, 2).reshape(pages * page, heads, dim)[~used]
+    assert kept.isnan().all()
+
+
+def test_cache_strided_rows_and_outputs():
+    cache = new_cache(4, 2, 16, 64, torch.bfloat16, True)
+    qkv = rand(10, 8, 64).bfloat16().to(DEV)  # one product's output: queries, then keys and values
+    slots = torch.arange(10, device=DEV) + 20
+    C.cache_write(cache, qkv[:, 4:6], qkv[:, 6:8], slots)
+    out = torch.full((10, 5, 70), 7.0, device=DEV).bfloat16()
+    k, v = C.cache_read(cache, slots, k=out[:, 1:3, 3:67], v=torch.empty(10, 2, 64, device=DEV).bfloat16())
+    other = new_cache(4, 2, 16, 64, torch.bfloat16, True)
+    C.cache_write(other, qkv[:, 4:6].contiguous(), qkv[:, 6:8].contiguous(), slots)
+    k2, v2 = C.cache_read(other, slots)
+    assert torch.equal(k, k2) and torch.equal(v, v2)
+    assert (out[:, 0] == 7).all() and (out[:, 3:] == 7).all() and (out[:, 1:3, :3] == 7).all() and (out[:, 1:3, 67:] == 7).all()
+
+
+def test_cache_special_rows():
+    x = rand(5, 1, 64)
+    x[0, 0, 3] = math.nan
+    x[1, 0, 4] = math.inf
+    x[2] *= 1e-38
+    x[3] = torch.finfo(torch.float32).max
+    cache = new_cache(1, 1, 8, 64, torch.float32, True)
+    slots = torch.arange(5, device=DEV)
+    C.cache_write(cache, x.to(DEV), x.to(DEV), slots)
+    back = C.cache_read(cache, slots, dtype=torch.float32)[0].cpu()
+    assert back[0].isnan().all() and back[1].isnan().all()
+    # the scale is its lower limit 2^-126: still half an e4m3 step everywhere
+    within(back[2], x[2].double(), quantised_bound(x[2].double(), torch.full((1,), 2.0 ** -126, dtype=torch.float64)), "tiny row")
+    assert ((back[3] - x[3]).abs() <= x[3] * 2.0 ** -4).all()
+    within(back[4], x[4].double(), quantised_bound(x[4].double(), x[4].double().abs().amax(-1) / 448), "row")
+
+
+# ---------------------------------------------------------------- attention
+
+
+def paged(k, v, lengths, page, t, quantised, seed=0, spare=3, token_major=False, bad=()):
+    """A cache holding k and v [B, HKV, L, D], its scattered pages, and the table."""
+    B, H, L, D = k.shape
+    width = max(1, -(-L // page))
+    pages = B * width + spare
+    cache = new_cache(pages, H, page, D, t, quantised, token_major)
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(seed))[:B * width].view(B, width).to(torch.int32)
+    tb = table.to(DEV)
+    for b in range(B):
+        n = int(lengths[b])
+        if n > 0:
+            pos = torch.arange(n, device=DEV)
+            slots = C.cache_slots(tb, torch.full_like(pos, b), pos, page)
+            C.cache_write(cache, k[b, :, :n].transpose(0, 1).contiguous().to(DEV), v[b, :, :n].transpose(0, 1).contiguous().to(DEV), slots)
+    for b, i, page_id in bad:
+        table[b, i] = page_id
+    return cache, table.to(DEV)
+
+
+def check_attend(B, heads, kv, D, page, lengths, dt, quantised, route="auto", seed=0, bad=(), token_major=False, scale=None,
+                 max_length=None, expect=None, q_scale=2.0):
+    print(f"attend B {B} heads {heads}/{kv} D {D} page {page} lengths {lengths} {dt} quantised {quantised} {route}", flush=True)
+    t = TYPES[dt]
+    L = max(1, max(lengths))
+    q = rand(B, heads, D, seed=seed, scale=q_scale).to(t)
+    k, v = rand(B, kv, L, D, seed=seed + 1).to(t), rand(B, kv, L, D, seed=seed + 2).to(t)
+    lens = torch.tensor(lengths, dtype=torch.int32)
+    cache, table = paged(k, v, lengths, page, t, quantised, seed, token_major=token_major, bad=bad)
+    qd = q.to(DEV)
+    p, info = C.attend_plan(cache, qd, table, scale, max_length, None, route)
+    if expect:
+        assert {n: c for c, n in ((1, "direct"), (2, "mfma"))}[expect] == info.route
+    out, lse = C.decode_attention(qd, cache, table, lens.to(DEV), scale=scale, lse=True, max_length=max_length, route=route)
+    torch.cuda.synchronize()
+    seen = torch.ones(B, table.shape[1] * page, dtype=torch.bool)
+    for b, i, page_id in bad:
+        seen[b, i * page:(i + 1) * page] = False
+    if max_length is not None:
+        lens = lens.clamp(max=max_length)
+    sc = D ** -0.5 if scale is None else scale
+    kr, vr = plain_rows(k, quantised), plain_rows(v, quantised)
+    want, want_lse, mag, top = attend64(q, kr, vr, lens, sc, seen)
+    # p meets V in float32 (direct), as float16, or as the sum of two bfloat16 values
+    p_step = 2.0 ** -11 if dt == "f16" and not quantised else 2.0 ** -15
+    bound = attend_bound(want, mag, top, D, L, t, p_step)
+    if dt == "f16":
+        bound = bound + L * 2.0 ** -25 * vr.abs().max()  # p below float16's smallest step
+    within(out, want, bound, "out")
+    within(lse, want_lse, ((D + 12) * U * top + (L / 4 + 64) * U + 4 * U * want_lse.abs().nan_to_num(0, 0, 0)), "lse")
+    return out
+
+
+LENGTHS = [[0], [1], [15, 16, 17], [31, 32, 33, 0, 1], [127, 128, 129], [255, 256, 257], [1000, 3, 0, 513]]
+
+
+@pytest.mark.parametrize("lengths", LENGTHS, ids=lambda v: "-".join(map(str, v)))
+@pytest.mark.parametrize("dt,quantised", [("bf16", False), ("bf16", True), ("f16", False), ("f16", True), ("f32", False), ("f32", True)])
+def test_attend_lengths(dt, quantised, lengths):
+    check_attend(len(lengths), 8, 2, 128, 16, lengths, dt, quantised)
+
+
+@pytest.mark.parametrize("D", [8, 16, 32, 48, 64, 80, 96, 112, 128, 160, 192, 240, 256, 264, 512, 33, 1])
+@pytest.mark.parametrize("dt,quantised", [("bf16", False), ("f16", True)])
+def test_attend_head_dims(dt, quantised, D):
+    check_attend(3, 4, 2, D, 16, [70, 1, 300], dt, quantised)
+
+
+@pytest.mark.parametrize("heads,kv", [(1, 1), (3, 3), (5, 1), (8, 8), (16, 1), (17, 1), (40, 2), (64, 2), (96, 1)])
+@pytest.mark.parametrize("quantised", [False, True])
+def test_attend_head_sharing(heads, kv, quantised):
+    check_attend(2, heads, kv, 64, 32, [100, 333], "bf16", quantised)
+
+
+@pytest.mark.parametrize("page", [1, 3, 8, 16, 24, 48, 64, 128, 256])
+@pytest.mark.parametrize("quantised", [False, True])
+def test_attend_page_sizes(page, quantised):
+    check_attend(3, 4, 2, 64, page, [1, 77, 530], "f16", quantised)
+
+
+@pytest.mark.parametrize("dt,quantised,route", [("bf16", True, "auto"), ("f16", False, "auto"), ("bf16", False, "direct"), ("f32", True, "auto")])
+def test_attend_long_is_split_and_joined(dt, quantised, route):
+    check_attend(2, 4, 1, 64, 64, [9001, 1200], dt, quantised, route)
+
+
+@pytest.mark.parametrize("route", ["auto", "direct"])
+@pytest.mark.parametrize("quantised", [False, True])
+def test_attend_pages_outside_the_cache_are_left_out(route, quantised):
+    for page in (16, 32):
+        check_attend(3, 4, 2, 64, page, [90, 40, 16], "bf16", quantised, route,
+                     bad=[(0, 1, -1), (0, 2, 2 ** 30), (1, 0, -2 ** 31), (2, 0, 10 ** 6)])
+
+
+def test_attend_options():
+    check_attend(2, 4, 2, 128, 16, [50, 60], "bf16", False, token_major=True)
+    check_attend(2, 4, 2, 128, 16, [50, 60], "bf16", True, token_major=True)
+    check_attend(2, 4, 2, 64, 16, [500, 60], "f16", True, max_length=77)
+    check_attend(2, 4, 2, 64, 16, [500, -5], "bf16", True, scale=-0.3)
+    check_attend(2, 4, 2, 64, 16, [500, 60], "bf16", False, scale=0.0)
+    # large scores: the running maximum has to carry the sums
+    check_attend(2, 4, 2, 64, 16, [700, 60], "bf16", False, q_scale=60.0)
+
+
+@pytest.mark.parametrize("route", ["auto", "direct"])
+def test_attend_special_scores(route):
+    """Keys of the type's lowest value and infinities that are seen: weights of 0, or NaN, as the formula gives."""
+    B, D, n = 1, 64, 40
+    q = torch.ones(B, 1, D).bfloat16()
+    k, v = rand(B, 1, n, D).bfloat16(), rand(B, 1, n, D, seed=9).bfloat16()
+    k[0, 0, :20] = torch.finfo(torch.bfloat16).min
+    k[0, 0, 25] = -math.inf
+    cache, table = paged(k, v, [n], 16, torch.bfloat16, False)
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    out = C.decode_attention(q.to(DEV), cache, table, lens, route=route).cpu()
+    keep = [i for i in range(20, n) if i != 25]
+    want, _, mag, top = attend64(q, k.double()[:, :, keep], v.double()[:, :, keep], [len(keep)], D ** -0.5)
+    within(out, want, attend_bound(want, mag, top, D, n, torch.bfloat16, 2.0 ** -15), "lowest keys")
+    k[0, 0, 30, 5] = math.nan
+    cache, table = paged(k, v, [n], 16, torch.bfloat16, False)
+    assert C.decode_attention(q.to(DEV), cache, table, lens, route=route).isnan().all()
+
+
+def test_attend_given_output_workspace_and_spacing():
+    D, B, H = 64, 3, 4
+    k, v = rand(B, 2, 600, D).bfloat16(), rand(B, 2, 600, D, seed=1).bfloat16()
+    lens = [600, 20, 0]
+    cache, table = paged(k, v, lens, 16, torch.bfloat16, True)
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    wide = rand(B, 10, D).bfloat16().to(DEV)
+    q = wide[:, 2:6]
+    ref, ref_lse = C.decode_attention(q.contiguous(), cache, table, ln, lse=True)
+    out = torch.full((B, 6, 72), 5.0, device=DEV).bfloat16()
+    big_table = torch.full((B, table.shape[1] + 7), -1, dtype=torch.int32, device=DEV)
+    big_table[:, :table.shape[1]] = table
+    _, info = C.attend_plan(cache, q, table)
+    ws = torch.full((info.workspace_bytes + 64,), 255, dtype=torch.uint8, device=DEV)
+    lse = torch.empty(B, H, device=DEV)
+    got, got_lse = C.decode_attention(q, cache, big_table[:, :table.shape[1]], ln, out=out[:, 1:5, 4:68], lse=lse, workspace=ws)
+    assert torch.equal(got, ref) and torch.equal(got_lse, ref_lse) and got_lse is lse
+    assert (out[:, 0] == 5).all() and (out[:, 5] == 5).all() and (out[:, :, :4] == 5).all() and (out[:, :, 68:] == 5).all()
+    assert (ws[info.workspace_bytes:] == 255).all()
+    # a query that is not 16-byte aligned runs the general kernel
+    odd = torch.empty(B * H * D + 1, device=DEV, dtype=torch.bfloat16)[1:].view(B, H, D)
+    odd.copy_(q)
+    got = C.decode_attention(odd, cache, table, ln)
+    assert (got.float() - ref.float()).abs().max() <= 2.0 ** -6 * ref.float().abs().max()
+
+
+def test_attend_refuses():
+    cache = new_cache(4, 2, 16, 64, torch.bfloat16, False, fill=0.0)
+    q = torch.zeros(2, 4, 64, device=DEV).bfloat16()
+    table, lens = torch.zeros(2, 2, dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+    for bad in [lambda: C.decode_attention(q.half(), cache, table, lens),
+                lambda: C.decode_attention(q[:, :, :32], cache, table, lens),
+                lambda: C.decode_attention(q, cache, table.long(), lens),
+                lambda: C.decode_attention(q, cache, table[:1], lens),
+                lambda: C.decode_attention(q, cache, table, lens[:1]),
+                lambda: C.decode_attention(q, cache, table, lens.long()),
+                lambda: C.decode_attention(q, cache, table, lens.cpu()),
+                lambda: C.decode_attention(q, cache, table, lens, out=q.float()),
+                lambda: C.decode_attention(q, cache, table, lens, lse=torch.zeros(2, 3, device=DEV)),
+                lambda: C.cache_write(cache, q[:, :2], q[:, :2], lens),
+                lambda: C.cache_write(cache, q, q, lens.long()),
+                lambda: C.cache_read(cache, lens.long(), dtype=torch.float16),
+                lambda: C.KVCache(cache.k, cache.v[:, :, :8]),
+                lambda: C.KVCache(cache.k, cache.v, torch.zeros(4, 2, 16, device=DEV), torch.zeros(4, 2, 16, device=DEV))]:
+        with pytest.raises(ValueError):
+            bad()
+    for bad in [lambda: C.decode_attention(q[:, :3], cache, table, lens),
+                lambda: C.decode_attention(q, cache, table, lens, max_length=33),
+                lambda: C.decode_attention(q, cache, table, lens, scale=math.inf)]:
+        with pytest.raises(C.ConvtError):
+            bad()
+    # an empty batch, a table of no pages, a cache of no pages
+    assert C.decode_attention(q[:0], cache, table[:0], lens[:0]).shape == (0, 4, 64)
+    assert (C.decode_attention(q, cache, table[:, :0], lens + 5) == 0).all()
+    empty = C.KVCache(cache.k[:0], cache.v[:0])
+    out, lse = C.decode_attention(q, empty, table, lens + 5, lse=True)
+    assert (out == 0).all() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("quantised", [True, False])
+def test_offsets_past_32_bits(quantised):
+    """Pages whose first element lies beyond 2^32 elements."""
+    heads, page, D = 8, 64, 256
+    pages = 2 ** 32 // (heads * page * D) + 40
+    t = torch.bfloat16
+    kind = E4M3 if quantised else t
+    k, v = (torch.empty(pages, heads, page, D, dtype=torch.uint8 if quantised else t, device=DEV) for _ in range(2))
+    k, v = (a.view(kind) for a in (k, v))
+    sc = [torch.empty(pages, heads, page, device=DEV) for _ in range(2)] if quantised else [None, None]
+    cache = C.KVCache(k, v, *sc)
+    n = 150
+    ids = torch.tensor([[pages - 1, 3, pages - 7]], dtype=torch.int32, device=DEV)
+    pos = torch.arange(n, device=DEV)
+    slots = C.cache_slots(ids, torch.zeros_like(pos), pos, page)
+    kk, vv = rand(n, heads, D).to(t), rand(n, heads, D, seed=1).to(t)
+    C.cache_write(cache, kk.to(DEV), vv.to(DEV), slots)
+    rk, rv = C.cache_read(cache, slots, dtype=t)
+    want_k, want_v = plain_rows(kk, quantised), plain_rows(vv, quantised)
+    within(rk, want_k, rounding(t, want_k) + want_k.abs() * 2 * U, "k")
+    within(rv, want_v, rounding(t, want_v) + want_v.abs() * 2 * U, "v")
+    q = rand(1, 16, D, seed=2).to(t)
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    for route in ("auto", "direct"):
+        out = C.decode_attention(q.to(DEV), cache, ids, lens, route=route)
+        want, _, mag, top = attend64(q, want_k.transpose(0, 1)[None], want_v.transpose(0, 1)[None], [n], D ** -0.5)
+        within(out, want, attend_bound(want, mag, top, D, n, t, 2.0 ** -15), route)
+
+
+# ---------------------------------------------------------------- 4-bit products
+
+
+def check_q4(rows, n, k, group, dt, x8, route="auto", seed=0, strided=False):
+    print(f"q4 rows {rows} n {n} k {k} group {group} {dt} x8 {x8} {route}", flush=True)
+    t = TYPES[dt]
+    g = torch.Generator().manual_seed(seed + rows + n + k)
+    w = torch.randint(0, 256, (n, k // 2), generator=g, dtype=torch.uint8)
+    scales = (0.02 * (0.5 + torch.rand(n, k // group, generator=g))).to(t)
+    x = torch.randn(rows, k, generator=g)
+    if x8:
+        xs = (x.abs().amax(-1) / 448).clamp(min=2.0 ** -126)
+        x = (x / xs.unsqueeze(-1)).to(E4M3)
+    else:
+        x, xs = x.to(t), None
+    xd = x.to(DEV)
+    y = None
+    if strided:
+        wide = torch.zeros(rows, k + 32, device=DEV, dtype=torch.uint8 if x8 else t)
+        wide = wide.view(E4M3) if x8 else wide
+        wide.view(torch.uint8 if x8 else t)[:, 16:16 + k] = xd.view(torch.uint8) if x8 else xd
+        xd = wide[:, 16:16 + k]
+        y = torch.full((rows, n + 3), 9.0, device=DEV).to(t)
+    got = C.q4_matvec(xd, w.to(DEV), scales.to(DEV), x_scale=None if xs is None else xs.to(DEV), route=route,
+                      y=None if y is None else y[:, 2:2 + n])
+    torch.cuda.synchronize()
+    wf = (torch.stack([w & 15, w >> 4], -1).reshape(n, k).double() - 8) * scales.double().repeat_interleave(group, 1)
+    xf = x.double() * (1 if xs is None else xs.double().unsqueeze(-1))
+    want = xf @ wf.t()
+    # the matrix cores see w + 16 (at most 31) and take 24 times the sum of x off again
+    mag = xf.abs() @ scales.double().repeat_interleave(group, 1).t() * 32
+    within(got, want, rounding(t, want) * (1 + 2.0 ** -6) + mag * (k / 64 + 64) * U, "y")
+    if y is not None:
+        assert (y[:, :2] == 9).all() and (y[:, n + 2:] == 9).all()
+
+
+@pytest.mark.parametrize("dt,x8", [("bf16", False), ("bf16", True), ("f16", False), ("f16", True), ("f32", False), ("f32", True)])
+@pytest.mark.parametrize("group", [8, 32, 64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 3])
+def test_q4_types_and_groups(dt, x8, group, rows):
+    check_q4(rows, 37, 768, group, dt, x8)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 4, 5, 15, 16, 17, 31, 33, 64, 65, 130])
+def test_q4_rows(rows):
+    check_q4(rows, 50, 512, 128, "bf16", rows % 2 == 0)
+
+
+@pytest.mark.parametrize("n", [1, 15, 16, 17, 63, 64, 65, 1000])
+@pytest.mark.parametrize("k,group", [(32, 32), (96, 32), (64, 64), (192, 64), (128, 128), (384, 128), (2048, 32), (4224, 128)])
+def test_q4_sizes(n, k, group):
+    check_q4(2, n, k, group, "f16" if n % 2 else "bf16", False)
+
+
+@pytest.mark.parametrize("rows", [1, 16, 20])
+def test_q4_large(rows):
+    check_q4(rows, 3000, 8192, 128, "bf16", rows == 16)
+    check_q4(rows, 4100, 2048, 64, "f16", False, strided=True)
+    check_q4(rows, 300, 4096, 32, "bf16", True, strided=True)
+
+
+def test_q4_alignment_and_leading_axes():
+    w, s = C.q4_quantise(rand(40, 256).bfloat16(), 64)
+    x = rand(6, 256).bfloat16().to(DEV)
+    wd, sd = w.to(DEV), s.to(DEV)
+    ref = C.q4_matvec(x, wd, sd)
+    lim = 2.0 ** -7 * ref.float().abs().max().item()
+    odd = torch.empty(6 * 256 + 1, dtype=torch.bfloat16, device=DEV)[1:].view(6, 256)
+    odd.copy_(x)
+    assert (C.q4_matvec(odd, wd, sd).float() - ref.float()).abs().max() <= lim
+    wo = torch.empty(40 * 128 + 3, dtype=torch.uint8, device=DEV)[3:].view(40, 128)
+    wo.copy_(wd)
+    assert (C.q4_matvec(x, wo, sd).float() - ref.float()).abs().max() <= lim
+    assert torch.equal(C.q4_matvec(x.view(2, 3, 256), wd, sd).view(6, 40), ref)
+    assert C.q4_matvec(x[0], wd, sd).shape == (40,)
+    assert C.q4_matvec(x[:0], wd, sd).shape == (0, 40)
+    # no k at all: sums of nothing
+    none = C.q4_matvec(x[:, :0], wd[:, :0].contiguous(), sd[:, :0].contiguous())
+    assert none.shape == (6, 40) and (none == 0).all()
+
+
+def test_q4_special_values():
+    w, s = C.q4_quantise(rand(16, 128).bfloat16(), 32)
+    x = rand(3, 128).bfloat16()
+    x[1, 5] = math.nan
+    y = C.q4_matvec(x.to(DEV), w.to(DEV), s.to(DEV))
+    assert y[1].isnan().all() and y[[0, 2]].isfinite().all()
+
+
+def test_q4_refuses():
+    x = torch.zeros(2, 64, device=DEV).bfloat16()
+    w, s = torch.zeros(4, 32, dtype=torch.uint8, device=DEV), torch.zeros(4, 2, device=DEV).bfloat16()
+    for bad in [lambda: C.q4_matvec(x[:, :32], w, s), lambda: C.q4_matvec(x.half(), w, s),
+                lambda: C.q4_matvec(x, w.to(torch.int8), s), lambda: C.q4_matvec(x, w, s[:3]),
+                lambda: C.q4_matvec(x, w[:, ::2], s), lambda: C.q4_matvec(x, w, s, x_scale=torch.ones(2, device=DEV)),
+                lambda: C.q4_matvec(x.to(E4M3), w, s), lambda: C.q4_matvec(x.to(E4M3), w, s, x_scale=torch.ones(3, device=DEV)),
+                lambda: C.q4_matvec(x, w, s, y=torch.zeros(2, 4, device=DEV)), lambda: C.q4_matvec(x, w.cpu(), s)]:
+        with pytest.raises(ValueError):
+            bad()
+
+
+# ---------------------------------------------------------------- streams and graphs
+
+
+def step(state, stream=None):
+    """One layer's token step through every operator."""
+    y, ys, h = C.rms_norm(state["x"], state["nw"], residual=state["h"], quantise=True, stream=stream)
+    qkv = C.q4_matvec(y, state["w"], state["s"], x_scale=ys, stream=stream).view(-1, 8, 64)
+    C.cache_write(state["cache"], qkv[:, 4:6], qkv[:, 6:8], state["slots"], stream=stream)
+    out = C.decode_attention(qkv[:, :4], state["cache"], state["table"], state["lens"], stream=stream)
+    k, v = C.cache_read(state["cache"], state["slots"], dtype=torch.bfloat16, stream=stream)
+    return y, ys, h, out, k, v
+
+
+def make_state(B=3, length=700):
+    kv = [rand(B, 2, length, 64, seed=s).bfloat16() for s in (1, 2)]
+    lens = [length, 40, 1]
+    cache, table = paged(*kv, [length - 1, 39, 0], 16, torch.bfloat16, True)
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    slots = C.cache_slots(table, torch.arange(B, device=DEV), (ln - 1).long(), 16)
+    w, s = C.q4_quantise(rand(512, 256, scale=0.1).bfloat16(), 64)
+    return dict(x=rand(B, 256).bfloat16().to(DEV), h=rand(B, 256, seed=5).bfloat16().to(DEV), nw=torch.ones(256, device=DEV).bfloat16(),
+                w=w.to(DEV), s=s.to(DEV), cache=cache, table=table, lens=ln, slots=slots)
+
+
+def same(a, b):
+    return all(torch.equal(x.float(), y.float()) for x, y in zip(a, b))
+
+
+def test_step_on_another_stream():
+    state = make_state()
+    want = step(state)
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    for _ in range(5):
+        got = step(state, stream=other)
+        junk = [torch.full((3, 4096), 3.0, device=DEV) for _ in range(8)]  # memory of freed outputs would be taken here
+        other.synchronize()
+        assert same(got, want)
+    got = step(state, stream=other.cuda_stream)
+    other.synchronize()
+    assert same(got, want)
+    del junk
+
+
+def test_step_in_a_graph():
+    state = make_state()
+    want = step(state)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(state)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(state)
+    x = state["x"].clone()
+    for i in range(4):
+        # new inputs in the captured buffers; the eager result of the same inputs
+        state["x"].copy_(x * (1 + i))
+        graph.replay()
+        torch.cuda.synchronize()
+        held = [t.clone() for t in got]
+        eager = step(state)
+        torch.cuda.synchronize()
+        assert same(held, eager), i
+    state["x"].copy_(x)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert same(got, want)
+
+
+def test_results_repeat():
+    """No result depends on the order in which blocks run."""
+    state = make_state()
+    want = step(state)
+    for _ in range(10):
+        assert same(step(state), want)
