@@ -96,7 +96,6 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Whether the MFMA attention kernel serves a problem (pointers apart).
 bool attend_mfma_serves(const convt_attend_problem &p) {
-    return false;
     const convt_cache_desc &c = p.cache;
     if (c.dtype == CONVT_DTYPE_F32 || c.head_dim % 16 != 0 || c.head_dim > 256 || c.page_size % 16 != 0) return false;
     const int64_t piece = c.quantised ? 16 : 8;  // elements in 16 bytes
@@ -149,9 +148,9 @@ convt_status attend_check(const convt_attend_problem *p, convt_attend_info *info
 
 // Whether the MFMA product kernel serves a problem (pointers apart).
 bool q4_mfma_serves(const convt_q4_problem &p) {
-    return false;
     if (p.dtype == CONVT_DTYPE_F32) return false;
     if (p.group != 32 && p.group != 64 && p.group != 128) return false;
+    if (p.rows > (1 << 20)) return false;  // the grid has an axis over rows
     return p.x_stride % 8 == 0 || p.rows <= 1;
 }
 
@@ -267,7 +266,10 @@ convt_status convt_attend(const convt_attend_problem *problem, const void *q, co
     a.div_page = convt::fast_div_of((uint32_t)c.page_size);
     a.div_heads = convt::fast_div_of((uint32_t)p.heads);
     const hipStream_t s = (hipStream_t)stream;
-    hipError_t e = convt::launch_attend_direct(a, c.dtype, c.quantised, s);
+    const bool mfma = info.route == CONVT_ATTEND_MFMA && aligned(q, 16) && aligned(k_cache, 16) &&
+                      aligned(v_cache, 16) && aligned(k_scale, 16) && aligned(v_scale, 16);
+    hipError_t e = mfma ? convt::launch_attend_mfma(a, c.dtype, c.quantised, s)
+                        : convt::launch_attend_direct(a, c.dtype, c.quantised, s);
     if (e == hipSuccess && a.chunks > 1) e = convt::launch_attend_join(a, c.dtype, s);
     return device_status(e);
 }
@@ -288,7 +290,9 @@ convt_status convt_q4_matvec(const convt_q4_problem *problem, const void *x, con
     if (!y || (p.x_quantised && !x_scale)) return CONVT_ERR_INVALID_ARGUMENT;
     if (p.k > 0 && (!x || !w || !scales)) return CONVT_ERR_INVALID_ARGUMENT;
     const hipStream_t s = (hipStream_t)stream;
-    return device_status(convt::launch_q4_direct(p, x, x_scale, w, scales, y, s));
+    const bool mfma = route == CONVT_Q4_MFMA && aligned(x, p.x_quantised ? 8 : 16) && aligned(w, 16);
+    return device_status(mfma ? convt::launch_q4_mfma(p, x, x_scale, w, scales, y, s)
+                              : convt::launch_q4_direct(p, x, x_scale, w, scales, y, s));
 }
 
 }  // extern "C"
