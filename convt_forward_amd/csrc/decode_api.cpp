@@ -122,15 +122,22 @@ convt_status attend_check(const convt_attend_problem *p, convt_attend_info *info
     const bool mfma = attend_mfma_serves(*p);
     if (p->route == CONVT_ATTEND_MFMA && !mfma) return CONVT_ERR_UNSUPPORTED;
     info->route = mfma && p->route != CONVT_ATTEND_DIRECT ? CONVT_ATTEND_MFMA : CONVT_ATTEND_DIRECT;
-    // Parts of the length axis: enough blocks to fill the card with the few
-    // rows that a batch has, parts of at least 256 tokens so that a block's
-    // start and the join stay small against its loads, and of at most 2048
-    // so that one long stream of a ragged batch is shared by many blocks.
+    // Parts of the length axis: as many blocks as the card holds at once (256
+    // CUs with 4, 3 or 1 of them, by the registers a head dimension takes) if
+    // every stream had max_length; parts of at least 128 tokens, a step of each
+    // wave. Streams differ, so parts are at most 512 tokens, that the blocks
+    // of a long stream need not run after all others have ended, but 1/64 of
+    // a long axis (up to 2048), where the join of more parts would cost more.
+    // Measured, us (parts of 128, 256, 512, 1024, 2048 tokens): 32 ragged streams
+    // up to 4096 x 8 kv heads, e4m3: 50, 41, 38, 37, 40; 4 streams of 100-131 K, bf16:
+    // 415, 369, 347, 334, 326; one stream of 60 K, one kv head of 256: 39, 27,
+    // 25, 32, 49; one of 3000, two heads, e4m3: 8.7, 9.3, 10.8, 14.4, 21.9.
     const int64_t items = (int64_t)p->batch * c.kv_heads;
-    const int64_t wanted = items > 0 ? ceil_div(1024, items) : 1;
-    int64_t chunk = ceil_div(ceil_div(p->max_length, wanted), 128) * 128;
-    if (chunk < 256) chunk = 256;
-    if (chunk > 2048) chunk = 2048;
+    const int64_t slots = 256 * (c.head_dim <= 64 ? 4 : c.head_dim <= 128 ? 3 : 1);
+    const int64_t longest = p->max_length / 64 < 512 ? 512 : p->max_length / 64 > 2048 ? 2048 : p->max_length / 64;
+    int64_t chunk = p->max_length / 128 * items / slots;  // steps of 128 tokens
+    chunk = chunk < 16 ? (chunk + 1) * 128 : 2048;
+    if (chunk > longest) chunk = (longest + 127) / 128 * 128;
     int64_t chunks = ceil_div(p->max_length, chunk);
     if (chunks < 1) chunks = 1;
     // the grid's second axis holds the parts
@@ -150,8 +157,9 @@ convt_status attend_check(const convt_attend_problem *p, convt_attend_info *info
 bool q4_mfma_serves(const convt_q4_problem &p) {
     if (p.dtype == CONVT_DTYPE_F32) return false;
     if (p.group != 32 && p.group != 64 && p.group != 128) return false;
-    if (p.rows > (1 << 20)) return false;  // the grid has an axis over rows
-    return p.x_stride % 8 == 0 || p.rows <= 1;
+    if (p.rows > (1 << 20)) return false;     // the grid has an axis over rows
+    if (p.k / p.group > 2000) return false;   // a tile's scales fit in 64 KB of LDS
+    return p.x_stride % (p.x_quantised ? 16 : 8) == 0 || p.rows <= 1;  // rows 16-byte aligned
 }
 
 convt_status q4_check(const convt_q4_problem *p, int32_t *route) {
@@ -290,7 +298,7 @@ convt_status convt_q4_matvec(const convt_q4_problem *problem, const void *x, con
     if (!y || (p.x_quantised && !x_scale)) return CONVT_ERR_INVALID_ARGUMENT;
     if (p.k > 0 && (!x || !w || !scales)) return CONVT_ERR_INVALID_ARGUMENT;
     const hipStream_t s = (hipStream_t)stream;
-    const bool mfma = route == CONVT_Q4_MFMA && aligned(x, p.x_quantised ? 8 : 16) && aligned(w, 16);
+    const bool mfma = route == CONVT_Q4_MFMA && aligned(x, 16) && aligned(w, 16);
     return device_status(mfma ? convt::launch_q4_mfma(p, x, x_scale, w, scales, y, s)
                               : convt::launch_q4_direct(p, x, x_scale, w, scales, y, s));
 }

@@ -134,14 +134,14 @@ __global__ __launch_bounds__(64 * kWaves) void attend_direct(AttendArgs a) {
 }
 
 // Joins the parts of one (stream, head): out = sum 2^(m_c - m) O_c / sum
-// 2^(m_c - m) l_c. The four waves take the parts in turn.
+// 2^(m_c - m) l_c. 4 dims a thread, 1 << lanes_log2 threads a part, the
+// block's other threads take other parts.
 template <typename T>
-__global__ __launch_bounds__(64 * kWaves) void attend_join(AttendArgs a) {
-    __shared__ float o_lds[kWaves][kMaxHeadDim];
-    __shared__ float r_lds[kWaves];
+__global__ __launch_bounds__(256) void attend_join(AttendArgs a, int lanes_log2) {
+    __shared__ float o_lds[256 * 4];
+    __shared__ float m_lds[kWaves], l_lds[256];
     const uint32_t b = fast_div(blockIdx.x, a.div_heads);
     const int h = (int)(blockIdx.x - b * (uint32_t)a.heads);
-    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
     int len = a.lengths[b];
     len = len < 0 ? 0 : len > a.max_length ? a.max_length : len;
     // part 0 is there even for an empty stream
@@ -151,39 +151,40 @@ __global__ __launch_bounds__(64 * kWaves) void attend_join(AttendArgs a) {
     const int64_t part0 = (int64_t)blockIdx.x * a.chunks;
     const float *ml = a.part_ml + part0 * 2;
     float m = -INFINITY;
-    for (int c = threadIdx.x; c < n; c += 64 * kWaves) m = fmaxf(m, ml[2 * c]);
+    for (int c = threadIdx.x; c < n; c += 256) m = fmaxf(m, ml[2 * c]);
     m = wave_max(m);
-    if (lane == 0) r_lds[wave] = m;
+    if (threadIdx.x % 64 == 0) m_lds[threadIdx.x / 64] = m;
     __syncthreads();
-    for (int w = 0; w < kWaves; ++w) m = fmaxf(m, r_lds[w]);
-    __syncthreads();
+    for (int w = 0; w < kWaves; ++w) m = fmaxf(m, m_lds[w]);
     const float base = m == -INFINITY ? 0.0f : m;
-    constexpr int NO = kMaxHeadDim / 64;
-    float o[NO] = {};
+    const int lanes = 1 << lanes_log2, groups = 256 >> lanes_log2;
+    const int d = (threadIdx.x & (lanes - 1)) * 4, group = threadIdx.x >> lanes_log2;
+    f32x4 o = {0, 0, 0, 0};
     float l = 0.0f;
-    for (int c = wave; c < n; c += kWaves) {
-        const float f = exp2f(ml[2 * c] - base);
-        l += ml[2 * c + 1] * f;
-        const float *p = a.part_o + (part0 + c) * D;
-#pragma unroll
-        for (int i = 0; i < NO; ++i) {
-            const int d = i * 64 + lane;
-            if (d < D) o[i] += p[d] * f;
+    if (d + 4 <= D) {
+#pragma unroll 4
+        for (int c = group; c < n; c += groups) {
+            const float f = __builtin_amdgcn_exp2f(ml[2 * c] - base);
+            l += ml[2 * c + 1] * f;
+            o += f * *(const f32x4_a4 *)(a.part_o + (part0 + c) * D + d);
+        }
+    } else if (d < D) {
+        for (int c = group; c < n; c += groups) {
+            const float f = __builtin_amdgcn_exp2f(ml[2 * c] - base);
+            l += ml[2 * c + 1] * f;
+            for (int j = 0; j < 3; ++j)
+                if (d + j < D) o[j] += f * a.part_o[(part0 + c) * D + d + j];
         }
     }
-#pragma unroll
-    for (int i = 0; i < NO; ++i) {
-        const int d = i * 64 + lane;
-        if (d < D) o_lds[wave][d] = o[i];
-    }
-    if (lane == 0) r_lds[wave] = l;
+    for (int j = 0; j < 4; ++j) o_lds[threadIdx.x * 4 + j] = o[j];
+    l_lds[threadIdx.x] = l;
     __syncthreads();
     l = 0.0f;
-    for (int w = 0; w < kWaves; ++w) l += r_lds[w];
-    for (int d = threadIdx.x; d < D; d += 64 * kWaves) {
+    for (int g = 0; g < groups; ++g) l += l_lds[g << lanes_log2];  // the lanes of a part agree
+    for (int i = threadIdx.x; i < D; i += 256) {
         float v = 0.0f;
-        for (int w = 0; w < kWaves; ++w) v += o_lds[w][d];
-        ((T *)a.out)[b * a.out_stride[0] + h * a.out_stride[1] + d] = from_f32<T>(l == 0.0f ? 0.0f : v / l);
+        for (int g = 0; g < groups; ++g) v += o_lds[(g << lanes_log2) * 4 + i];
+        ((T *)a.out)[b * a.out_stride[0] + h * a.out_stride[1] + i] = from_f32<T>(l == 0.0f ? 0.0f : v / l);
     }
     if (threadIdx.x == 0 && a.lse) a.lse[blockIdx.x] = (m + log2f(l)) * 0.69314718055994531f;
 }
@@ -205,9 +206,11 @@ hipError_t launch_attend_direct(const AttendArgs &a, int dtype, int quantised, h
 
 hipError_t launch_attend_join(const AttendArgs &a, int dtype, hipStream_t stream) {
     const unsigned grid = (unsigned)a.batch * (unsigned)a.heads;
-    if (dtype == CONVT_DTYPE_F32) attend_join<float><<<grid, 64 * kWaves, 0, stream>>>(a);
-    else if (dtype == CONVT_DTYPE_BF16) attend_join<uint16_t><<<grid, 64 * kWaves, 0, stream>>>(a);
-    else attend_join<_Float16><<<grid, 64 * kWaves, 0, stream>>>(a);
+    int lanes_log2 = 0;
+    while ((4 << lanes_log2) < a.head_dim) ++lanes_log2;
+    if (dtype == CONVT_DTYPE_F32) attend_join<float><<<grid, 256, 0, stream>>>(a, lanes_log2);
+    else if (dtype == CONVT_DTYPE_BF16) attend_join<uint16_t><<<grid, 256, 0, stream>>>(a, lanes_log2);
+    else attend_join<_Float16><<<grid, 256, 0, stream>>>(a, lanes_log2);
     return hipGetLastError();
 }
 

@@ -76,9 +76,10 @@ template <> struct Piece<8> { typedef u32x2 type; };
 template <> struct Piece<16> { typedef u32x4 type; };
 
 // E: type of q, out and of an unquantised cache. DP: head_dim rounded up to 64,
-// 128 or 256. FULL: head_dim == DP.
+// 128 or 256. FULL: head_dim == DP. The second launch bound is the blocks of
+// a CU that the registers are held to: 4, 3 and 1 by DP.
 template <typename E, bool Q8, int DP, bool FULL>
-__global__ __launch_bounds__(64 * kWaves) void attend_mfma(AttendArgs a, int head_tiles) {
+__global__ __launch_bounds__(64 * kWaves, DP == 64 ? 4 : DP == 128 ? 3 : 1) void attend_mfma(AttendArgs a, int head_tiles) {
     typedef typename std::conditional<Q8, __bf16, E>::type EV;  // P and V
     typedef typename Vec8<E>::type E8;
     typedef typename Vec8<EV>::type EV8;
@@ -136,17 +137,25 @@ __global__ __launch_bounds__(64 * kWaves) void attend_mfma(AttendArgs a, int hea
 
     // The pages of the two tiles of a step. A tile past the end takes the
     // last one there is; its tokens are masked by their index.
-    auto locate = [&](int ts) {
+    int32_t entry[2];
+    int entry_off[2];
+    auto look_up = [&](int ts) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             int t = ts + 16 * u;
             const int last = (t1 - 1) & ~15;
             t = t < last ? t : last;
             const int pi = (int)fast_div((uint32_t)t, a.div_page);
-            const int64_t p = table[pi];
-            ok[u] = p >= 0 && p < a.n_pages;
-            page[u] = ok[u] ? p : 0;
-            off[u] = t - pi * a.page_size;
+            entry[u] = table[pi];
+            entry_off[u] = t - pi * a.page_size;
+        }
+    };
+    auto take_entries = [&]() {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            ok[u] = entry[u] >= 0 && entry[u] < a.n_pages;
+            page[u] = ok[u] ? entry[u] : 0;
+            off[u] = entry_off[u];
         }
     };
     auto load_k = [&]() {
@@ -194,15 +203,21 @@ __global__ __launch_bounds__(64 * kWaves) void attend_mfma(AttendArgs a, int hea
 
     int ts = t0 + wave * kStep;
     if (ts < t1) {
-        locate(ts);
+        look_up(ts);
+        take_entries();
         load_scales();
         load_k();
         load_v();
     }
+    // The next step's loads are issued without a condition (past the end they
+    // read the last tile again, from the caches): the compiler's waits count
+    // the loads in flight on the path with the fewest, so a branch around
+    // them would make every wait one for all.
     for (; ts < t1; ts += kWaves * kStep) {
         const int next = ts + kWaves * kStep;
         const bool partial = ts + kStep > t1 || !ok[0] || !ok[1];
         const bool seen0 = ok[0], seen1 = ok[1];
+        look_up(next);
         f32x4 s[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -220,17 +235,19 @@ __global__ __launch_bounds__(64 * kWaves) void attend_mfma(AttendArgs a, int hea
                 s[u] = mfma16(__builtin_bit_cast(E8, w), q[c], s[u]);
             }
         }
+        // The phases of a step stay apart: mixed, their temporaries would not
+        // fit in the registers of the waves a SIMD should hold.
+        __builtin_amdgcn_sched_barrier(0);
         f32x4 vscale[2] = {vs[0], vs[1]};
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             s[u] *= a.scale_log2e;
             if constexpr (Q8) s[u] *= ks[u];
         }
-        if (next < t1) {
-            locate(next);
-            load_scales();
-            load_k();
-        }
+        take_entries();
+        load_scales();
+        load_k();
+        __builtin_amdgcn_sched_barrier(0);
         if (partial) {
             // unseen tokens: no weight, and their values (whatever they
             // hold) become 0
@@ -278,6 +295,7 @@ __global__ __launch_bounds__(64 * kWaves) void attend_mfma(AttendArgs a, int hea
         // V^T: two dims (one word of each token) at a time
 #pragma unroll
         for (int jw = 0; jw < VD / 2; ++jw) {
+            __builtin_amdgcn_sched_barrier(0);
             uint32_t w[8];
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
@@ -300,7 +318,8 @@ __global__ __launch_bounds__(64 * kWaves) void attend_mfma(AttendArgs a, int hea
                 o[2 * jw + 1] = mfma16(__builtin_bit_cast(EV8, hi), __builtin_bit_cast(EV8, pl), o[2 * jw + 1]);
             }
         }
-        if (next < t1) load_v();
+        __builtin_amdgcn_sched_barrier(0);
+        load_v();
     }
 
     // Join the waves: lane (head r, rows 4g + i) holds dims VD (4g + i) + j.

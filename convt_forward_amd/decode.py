@@ -21,7 +21,7 @@ from typing import Dict, Optional, Tuple
 
 import torch
 
-from . import ConvtError, DTYPES, _launch_stream, _tie_to_stream
+from . import ConvtError, DTYPES, _launch_stream as _given_stream, _tie_to_stream
 from . import lib as _load
 
 ATTEND_ROUTES = {"auto": 0, "direct": 1, "mfma": 2}
@@ -88,10 +88,16 @@ def lib() -> ctypes.CDLL:
     return _ready
 
 
-def _call(name: str, *args) -> None:
-    st = getattr(_ready or lib(), name)(*args)
-    if st != 0:
-        raise ConvtError(st, name)
+def _raise(st: int, name: str) -> None:
+    raise ConvtError(st, name)
+
+
+def _launch_stream(stream, device):
+    """_launch_stream of the package; the current stream's handle without making a Stream
+    object, which costs as much as the launch itself."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index), None
+    return _given_stream(stream, device)
 
 
 def _code(t, name: str) -> int:
@@ -190,8 +196,10 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, quantise: bool = False
     elif scale is not None:
         raise ValueError("scale without quantise")
     p = NormProblem(rows, width, xs, rs, ys, ros, code, 0 if residual is None else 1, 1 if quantise else 0, eps)
-    _call("convt_rms_norm", ctypes.byref(p), x.data_ptr(), weight.data_ptr(), _ptr(residual), y.data_ptr(), _ptr(scale),
+    st = (_ready or lib()).convt_rms_norm(ctypes.byref(p), x.data_ptr(), weight.data_ptr(), _ptr(residual), y.data_ptr(), _ptr(scale),
           _ptr(residual_out), sh)
+    if st:
+        _raise(st, "convt_rms_norm")
     _tie_to_stream(owned, ext)
     return y, scale, residual_out
 
@@ -282,8 +290,10 @@ def cache_write(cache: KVCache, k, v, slots, stream=None) -> KVCache:
     rows = _cache_rows(cache, k, v, slots)
     d = cache._desc(k.dtype, "k")
     sh, _ = _launch_stream(stream, cache.device)
-    _call("convt_cache_write", ctypes.byref(d), ctypes.byref(rows), k.data_ptr(), v.data_ptr(), slots.data_ptr(),
+    st = (_ready or lib()).convt_cache_write(ctypes.byref(d), ctypes.byref(rows), k.data_ptr(), v.data_ptr(), slots.data_ptr(),
           cache.k.data_ptr(), cache.v.data_ptr(), _ptr(cache.k_scale), _ptr(cache.v_scale), sh)
+    if st:
+        _raise(st, "convt_cache_write")
     return cache
 
 
@@ -308,8 +318,10 @@ def cache_read(cache: KVCache, slots, dtype=None, k=None, v=None, stream=None):
     if k.dtype != dtype:
         raise ValueError(f"k must be {dtype}")
     rows = _cache_rows(cache, k, v, slots)
-    _call("convt_cache_read", ctypes.byref(d), ctypes.byref(rows), cache.k.data_ptr(), cache.v.data_ptr(),
+    st = (_ready or lib()).convt_cache_read(ctypes.byref(d), ctypes.byref(rows), cache.k.data_ptr(), cache.v.data_ptr(),
           _ptr(cache.k_scale), _ptr(cache.v_scale), slots.data_ptr(), k.data_ptr(), v.data_ptr(), sh)
+    if st:
+        _raise(st, "convt_cache_read")
     _tie_to_stream(owned, ext)
     return k, v
 
@@ -349,7 +361,9 @@ def attend_plan(cache: KVCache, q, page_table, scale=None, max_length: Optional[
                       page_table.stride(0) if batch > 1 else max(1, width), batch, heads, ATTEND_ROUTES[route],
                       1.0 / math.sqrt(dim) if scale is None else scale)
     info = AttendInfo()
-    _call("convt_attend_query", ctypes.byref(p), ctypes.byref(info))
+    st = (_ready or lib()).convt_attend_query(ctypes.byref(p), ctypes.byref(info))
+    if st:
+        _raise(st, "convt_attend_query")
     if len(cache._attends) >= 256:
         cache._attends.clear()
     cache._attends[key] = (p, info)
@@ -398,9 +412,11 @@ def decode_attention(q, cache: KVCache, page_table, lengths, scale: Optional[flo
             owned.append(workspace)
     elif not workspace.is_cuda or workspace.numel() * workspace.element_size() < info.workspace_bytes:
         raise ValueError("workspace too small")
-    _call("convt_attend", ctypes.byref(p), q.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(), _ptr(cache.k_scale),
+    st = (_ready or lib()).convt_attend(ctypes.byref(p), q.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(), _ptr(cache.k_scale),
           _ptr(cache.v_scale), page_table.data_ptr(), lengths.data_ptr(), out.data_ptr(), _ptr(lse_t),
           _ptr(workspace), sh)
+    if st:
+        _raise(st, "convt_attend")
     _tie_to_stream(owned, ext)
     return out if lse_t is None else (out, lse_t)
 
@@ -460,7 +476,9 @@ def q4_matvec(x, w, scales, x_scale=None, y=None, stream=None, route: str = "aut
         _check(y, "y", shape, dtype, device)
         ys = _rows(y, "y")[1]
     p = Q4Problem(rows, n, k, k // groups if groups else 8, xs, ys, code, 1 if quantised else 0, Q4_ROUTES[route], 0)
-    _call("convt_q4_matvec", ctypes.byref(p), x.data_ptr(), _ptr(x_scale), w.data_ptr(), scales.data_ptr(),
+    st = (_ready or lib()).convt_q4_matvec(ctypes.byref(p), x.data_ptr(), _ptr(x_scale), w.data_ptr(), scales.data_ptr(),
           y.data_ptr(), sh)
+    if st:
+        _raise(st, "convt_q4_matvec")
     _tie_to_stream(owned, ext)
     return y

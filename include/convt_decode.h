@@ -188,7 +188,7 @@ convt_status convt_attend(const convt_attend_problem *problem, const void *q, co
  * strides of x >= k and of y >= n (read only when rows > 1); rows and k below
  * 2^31, n at most 2^26 - 4.
  * Routes: Q4_MFMA (two-byte types, group 32, 64 or 128, w and x rows 16-byte
- * aligned (e4m3 x: 8-byte)) on the matrix cores; Q4_DIRECT for everything
+ * aligned) on the matrix cores; Q4_DIRECT for everything
  * else, also at run time for pointers not so aligned.
  */
 typedef enum convt_q4_route {
