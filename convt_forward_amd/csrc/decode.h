@@ -25,7 +25,8 @@ struct CacheArgs {
     int64_t row_stride[2][2];     // [k, v][token, head]
     int64_t cache_stride[2][3];   // [k, v][page, head, token]
     int64_t n_slots;              // n_pages * page_size
-    uint32_t items;               // tokens * kv_heads
+    int64_t tokens;
+    uint32_t items;               // blocks of tokens * kv_heads (k_cache.hip)
     int32_t kv_heads, page_size, head_dim;
     FastDiv div_heads, div_page;
 };

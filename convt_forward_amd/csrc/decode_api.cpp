@@ -82,7 +82,7 @@ convt_status cache_move(const convt_cache_desc *cache, const convt_cache_rows *r
         a.cache_stride[1][i] = cache->v_stride[i];
     }
     a.n_slots = cache->n_pages * cache->page_size;
-    a.items = (uint32_t)(rows->tokens * cache->kv_heads);
+    a.tokens = rows->tokens;
     a.kv_heads = cache->kv_heads;
     a.page_size = cache->page_size;
     a.head_dim = cache->head_dim;

@@ -159,6 +159,34 @@ __device__ __forceinline__ float row_scale(uint32_t amax_bits, float &inv) {
     return s;
 }
 
+// The largest over the 1 << log2 neighbouring lanes of each of N values,
+// given to all of them: lane exchanges inside rows of 16 lanes by DPP, between
+// rows by the row swaps.
+template <int CTRL> __device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true);
+    return o > v ? o : v;
+}
+template <int N> __device__ __forceinline__ void group_max_u32(uint32_t (&v)[N], int log2) {
+    if (log2 > 0)
+        for (int i = 0; i < N; ++i) v[i] = max_dpp<0xb1>(v[i]);  // quad_perm 1, 0, 3, 2
+    if (log2 > 1)
+        for (int i = 0; i < N; ++i) v[i] = max_dpp<0x4e>(v[i]);  // quad_perm 2, 3, 0, 1
+    if (log2 > 2)
+        for (int i = 0; i < N; ++i) v[i] = max_dpp<0x141>(v[i]);  // row_half_mirror
+    if (log2 > 3)
+        for (int i = 0; i < N; ++i) v[i] = max_dpp<0x140>(v[i]);  // row_mirror
+    if (log2 > 4)
+        for (int i = 0; i < N; ++i) {
+            auto a = __builtin_amdgcn_permlane16_swap(v[i], v[i], false, false);
+            v[i] = a[0] > a[1] ? a[0] : a[1];
+        }
+    if (log2 > 5)
+        for (int i = 0; i < N; ++i) {
+            auto a = __builtin_amdgcn_permlane32_swap(v[i], v[i], false, false);
+            v[i] = a[0] > a[1] ? a[0] : a[1];
+        }
+}
+
 __device__ __forceinline__ float wave_sum(float v) {
     for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
     return v;
@@ -168,11 +196,9 @@ __device__ __forceinline__ float wave_max(float v) {
     return v;
 }
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-    for (int m = 32; m > 0; m >>= 1) {
-        const uint32_t o = (uint32_t)__shfl_xor((int)v, m);
-        v = o > v ? o : v;
-    }
-    return v;
+    uint32_t a[1] = {v};
+    group_max_u32(a, 6);
+    return a[0];
 }
 
 }  // namespace convt
