@@ -108,9 +108,10 @@ def _code(t, name: str) -> int:
 
 
 def _check(t, name: str, shape=None, dtype=None, device=None) -> None:
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if device is not None and t.device != device:
+    if device is None:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+    elif t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}")
@@ -141,6 +142,16 @@ def _rows(t, name: str) -> Tuple[int, int]:
     return rows, step if rows > 1 else width
 
 
+def _empty(shape, dtype, device):
+    """A new contiguous tensor. empty_strided skips most of what torch.empty does with its
+    arguments (1.3 against 2.1 us, a third of a small call)."""
+    stride, n = [], 1
+    for v in reversed(shape):
+        stride.append(n)
+        n *= v if v > 1 else 1
+    return torch.empty_strided(shape, stride[::-1], dtype=dtype, device=device)
+
+
 def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -169,7 +180,7 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, quantise: bool = False
         _check(residual, "residual", shape, dtype, device)
         rs = _rows(residual, "residual")[1]
         if residual_out is None:
-            residual_out = torch.empty(shape, dtype=dtype, device=device)
+            residual_out = _empty(shape, dtype, device)
             owned.append(residual_out)
             ros = width
         else:
@@ -179,7 +190,7 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, quantise: bool = False
         raise ValueError("residual_out without a residual")
     out_dtype = _E4M3 if quantise else dtype
     if y is None:
-        y = torch.empty(shape, dtype=out_dtype, device=device)
+        y = _empty(shape, out_dtype, device)
         owned.append(y)
         ys = width
     else:
@@ -187,7 +198,7 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, quantise: bool = False
         ys = _rows(y, "y")[1]
     if quantise:
         if scale is None:
-            scale = torch.empty(shape[:-1], dtype=torch.float32, device=device)
+            scale = _empty(shape[:-1], torch.float32, device)
             owned.append(scale)
         else:
             _check(scale, "scale", shape[:-1], torch.float32, device)
@@ -200,7 +211,8 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, quantise: bool = False
           _ptr(residual_out), sh)
     if st:
         _raise(st, "convt_rms_norm")
-    _tie_to_stream(owned, ext)
+    if ext is not None:
+        _tie_to_stream(owned, ext)
     return y, scale, residual_out
 
 
@@ -310,10 +322,10 @@ def cache_read(cache: KVCache, slots, dtype=None, k=None, v=None, stream=None):
         raise ValueError("slots must have one axis")
     sh, ext = _launch_stream(stream, cache.device)
     if k is None:
-        k = torch.empty(shape, dtype=dtype, device=cache.device)
+        k = _empty(shape, dtype, cache.device)
         owned.append(k)
     if v is None:
-        v = torch.empty(shape, dtype=dtype, device=cache.device)
+        v = _empty(shape, dtype, cache.device)
         owned.append(v)
     if k.dtype != dtype:
         raise ValueError(f"k must be {dtype}")
@@ -322,7 +334,8 @@ def cache_read(cache: KVCache, slots, dtype=None, k=None, v=None, stream=None):
           _ptr(cache.k_scale), _ptr(cache.v_scale), slots.data_ptr(), k.data_ptr(), v.data_ptr(), sh)
     if st:
         _raise(st, "convt_cache_read")
-    _tie_to_stream(owned, ext)
+    if ext is not None:
+        _tie_to_stream(owned, ext)
     return k, v
 
 
@@ -395,11 +408,11 @@ def decode_attention(q, cache: KVCache, page_table, lengths, scale: Optional[flo
     sh, ext = _launch_stream(stream, cache.device)
     owned = []
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=cache.device)
+        out = _empty(q.shape, q.dtype, cache.device)
         owned.append(out)
     lse_t = None
     if lse is True:
-        lse_t = torch.empty((batch, heads), dtype=torch.float32, device=cache.device)
+        lse_t = _empty((batch, heads), torch.float32, cache.device)
         owned.append(lse_t)
     elif lse is not False and lse is not None:
         _check(lse, "lse", (batch, heads), torch.float32, cache.device)
@@ -408,7 +421,7 @@ def decode_attention(q, cache: KVCache, page_table, lengths, scale: Optional[flo
         lse_t = lse
     if workspace is None:
         if info.workspace_bytes:
-            workspace = torch.empty(info.workspace_bytes, dtype=torch.uint8, device=cache.device)
+            workspace = _empty((info.workspace_bytes,), torch.uint8, cache.device)
             owned.append(workspace)
     elif not workspace.is_cuda or workspace.numel() * workspace.element_size() < info.workspace_bytes:
         raise ValueError("workspace too small")
@@ -417,7 +430,8 @@ def decode_attention(q, cache: KVCache, page_table, lengths, scale: Optional[flo
           _ptr(workspace), sh)
     if st:
         _raise(st, "convt_attend")
-    _tie_to_stream(owned, ext)
+    if ext is not None:
+        _tie_to_stream(owned, ext)
     return out if lse_t is None else (out, lse_t)
 
 
@@ -469,7 +483,7 @@ def q4_matvec(x, w, scales, x_scale=None, y=None, stream=None, route: str = "aut
     owned = []
     shape = x.shape[:-1] + (n,)
     if y is None:
-        y = torch.empty(shape, dtype=dtype, device=device)
+        y = _empty(shape, dtype, device)
         owned.append(y)
         ys = n
     else:
@@ -480,5 +494,6 @@ def q4_matvec(x, w, scales, x_scale=None, y=None, stream=None, route: str = "aut
           y.data_ptr(), sh)
     if st:
         _raise(st, "convt_q4_matvec")
-    _tie_to_stream(owned, ext)
+    if ext is not None:
+        _tie_to_stream(owned, ext)
     return y
