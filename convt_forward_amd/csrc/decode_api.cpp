@@ -29,9 +29,10 @@ constexpr int64_t kMaxIndex = ((int64_t)1 << 31) - 1;
 // threads in 32 bits).
 constexpr int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;
 
-bool strides_ok(const int64_t *s, int n) {
+// Strides of what is written are at least 1; what is only read may repeat (0).
+bool strides_ok(const int64_t *s, int n, int64_t least = 1) {
     for (int i = 0; i < n; ++i)
-        if (s[i] < 1 || s[i] > kMaxStride) return false;
+        if (s[i] < least || s[i] > kMaxStride) return false;
     return true;
 }
 
@@ -61,7 +62,7 @@ convt_status cache_move(const convt_cache_desc *cache, const convt_cache_rows *r
     if (st != CONVT_OK) return st;
     if (rows->tokens < 0 || rows->tokens > kMaxIndex || rows->tokens * cache->kv_heads > kMaxIndex)
         return CONVT_ERR_INVALID_ARGUMENT;
-    if (!strides_ok(rows->k_stride, 2) || !strides_ok(rows->v_stride, 2)) return CONVT_ERR_INVALID_ARGUMENT;
+    if (!strides_ok(rows->k_stride, 2, !write) || !strides_ok(rows->v_stride, 2, !write)) return CONVT_ERR_INVALID_ARGUMENT;
     if (!cache_pointers_ok(*cache, k_cache, v_cache, k_scale, v_scale)) return CONVT_ERR_INVALID_ARGUMENT;
     if (rows->tokens == 0) return CONVT_OK;
     if (!k || !v || !slots) return CONVT_ERR_INVALID_ARGUMENT;
@@ -116,7 +117,7 @@ convt_status attend_check(const convt_attend_problem *p, convt_attend_info *info
         return CONVT_ERR_INVALID_ARGUMENT;
     if (p->max_length < 0 || p->max_length > kMaxIndex - 4096 || p->max_length > p->table_width * c.page_size)
         return CONVT_ERR_INVALID_ARGUMENT;
-    if (!strides_ok(p->q_stride, 2) || !strides_ok(p->out_stride, 2)) return CONVT_ERR_INVALID_ARGUMENT;
+    if (!strides_ok(p->q_stride, 2, 0) || !strides_ok(p->out_stride, 2)) return CONVT_ERR_INVALID_ARGUMENT;
     if (!isfinite(p->scale)) return CONVT_ERR_INVALID_ARGUMENT;
     if (p->route < CONVT_ATTEND_AUTO || p->route > CONVT_ATTEND_MFMA) return CONVT_ERR_INVALID_ARGUMENT;
     const bool mfma = attend_mfma_serves(*p);

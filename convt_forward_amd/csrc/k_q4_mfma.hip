@@ -406,8 +406,8 @@ template <typename E, bool X8, int GS, int NT, int MT> void go(Q4Args a, int wk,
         a.x_at = (int)scales;
         a.x_row = stages * U * 128 * (X8 ? 1 : 2) + 64;
         const size_t x = (size_t)a.rows * a.x_row;
-        if (x <= kXLds) {
-            const size_t all = scales + x;
+        const size_t all = scales + x;
+        if (x <= kXLds && all <= 65536) {
             q4_mfma<E, X8, GS, NT, MT, U, true><<<grid, 64 * wk * wn, all > sums ? all : sums, s>>>(a);
             return;
         }

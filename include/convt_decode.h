@@ -27,7 +27,8 @@
  * codes that are 0 or NaN: both read back as NaN in every place.
  *
  * Problem structs are zero-initialised by the caller and then filled;
- * fields named reserved must be 0. Strides count elements.
+ * fields named reserved must be 0. Strides count elements; those of what a call
+ * only reads may be 0 (a repeated row), others are at least 1, none above 2^40.
  */
 #ifndef CONVT_DECODE_H
 #define CONVT_DECODE_H
@@ -127,7 +128,7 @@ convt_status convt_cache_read(const convt_cache_desc *cache, const convt_cache_r
  * it holds.
  *
  * max_length bounds the lengths the call handles: at most table_width *
- * page_size. The length axis is cut into chunks that are computed by different
+ * page_size, and below 2^31 - 4096. The length axis is cut into chunks that are computed by different
  * blocks and joined by a second kernel through the workspace; with one chunk
  * there is one kernel and no workspace.
  *
@@ -179,7 +180,8 @@ convt_status convt_attend(const convt_attend_problem *problem, const void *q, co
  * Products of a few rows with 4-bit weights:
  *     y[m, n] = x_scale[m] * sum_g scales[n, g] * sum_{k in group g} x[m, k] * (w[n, k] - 8)
  * w: [n][k / 2] bytes, the even k in the low four bits, values 0 .. 15 that
- * stand for -8 .. 7; scales [n][k / group] of the element type; both
+ * stand for -8 .. 7 (a row of x that holds an infinity or NaN gives results that
+ * are not finite either); scales [n][k / group] of the element type; both
  * contiguous. x is [rows][k] of the element type, or, with x_quantised = 1,
  * e4m3 codes with x_scale float32 [rows] (the norm's quantised output;
  * x_scale is left out otherwise). y is [rows][n] of the element type. Sums in

@@ -70,11 +70,13 @@ def test_cache_refuses(which):
     for kw in BAD_CACHE:
         assert move(which, desc(**kw)) == 1, kw
     for kw in [dict(tokens=-1), dict(tokens=2 ** 31), dict(tokens=2 ** 30), dict(k=None), dict(v=None),
-               dict(slots=None), dict(kc=None), dict(vc=None), dict(ks=FAKE), dict(vs=FAKE), dict(rk=(0, 64)),
+               dict(slots=None), dict(kc=None), dict(vc=None), dict(ks=FAKE), dict(vs=FAKE), dict(rk=(-1, 64)),
                dict(rv=(128, -64))]:
         assert move(which, desc(), **kw) == 1, kw
     for kw in [dict(), dict(ks=FAKE), dict(vs=FAKE)]:
         assert move(which, desc(q=1), **kw) == 1, kw
+    if which == "read":  # written rows may not coincide
+        assert move(which, desc(), rk=(0, 64)) == 1 and move(which, desc(), rv=(128, 0)) == 1
     assert move(which, desc(dim=513)) == 2
     assert move(which, desc(dtype=3)) == 2
     assert move(which, desc(), tokens=0, k=None, v=None, slots=None) == 0
@@ -94,7 +96,7 @@ def query(**kw):
 
 
 @pytest.mark.parametrize("kw", BAD_CACHE + [
-    dict(max_length=-1), dict(max_length=65), dict(qs=(0, 64)), dict(os_=(256, -1)), dict(width=-1), dict(stride=3),
+    dict(max_length=-1), dict(max_length=65), dict(qs=(-1, 64)), dict(os_=(256, 0)), dict(width=-1), dict(stride=3),
     dict(batch=-1), dict(heads=0), dict(heads=3), dict(route=3), dict(route=-1), dict(scale=float("nan")),
     dict(scale=float("inf")), dict(max_length=2 ** 31 - 1, width=2 ** 30, stride=2 ** 30)])
 def test_attend_refuses(kw):

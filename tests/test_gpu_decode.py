@@ -362,6 +362,22 @@ def test_attend_given_output_workspace_and_spacing():
     assert (got.float() - ref.float()).abs().max() <= 2.0 ** -6 * ref.float().abs().max()
 
 
+def test_repeated_inputs():
+    """Rows that are one row in memory (stride 0), where they are only read."""
+    cache = new_cache(4, 2, 16, 64, torch.bfloat16, True)
+    one = rand(1, 1, 64).bfloat16().to(DEV)
+    slots = torch.arange(30, device=DEV)
+    C.cache_write(cache, one.expand(30, 2, 64), one.expand(30, 2, 64), slots)
+    k, v = C.cache_read(cache, slots)
+    assert torch.equal(k, k[:1, :1].expand_as(k)) and torch.equal(v, k)
+    table = torch.arange(2, dtype=torch.int32, device=DEV).view(1, 2)
+    lens = torch.tensor([30], dtype=torch.int32, device=DEV)
+    out = C.decode_attention(one.expand(1, 4, 64), cache, table, lens)
+    assert (out.float() - k[0, 0].float()).abs().max() <= 2.0 ** -7 * k.float().abs().max()
+    both = C.decode_attention(one.expand(2, 4, 64), cache, table.expand(2, 2).contiguous(), lens.repeat(2))
+    assert torch.equal(both[0], both[1]) and torch.equal(both[:1], out)
+
+
 def test_attend_refuses():
     cache = new_cache(4, 2, 16, 64, torch.bfloat16, False, fill=0.0)
     q = torch.zeros(2, 4, 64, device=DEV).bfloat16()
@@ -483,6 +499,14 @@ def test_q4_large(rows):
     check_q4(rows, 3000, 8192, 128, "bf16", rows == 16)
     check_q4(rows, 4100, 2048, 64, "f16", False, strided=True)
     check_q4(rows, 300, 4096, 32, "bf16", True, strided=True)
+
+
+@pytest.mark.parametrize("rows,n,k,group", [(1, 16400, 12288, 32), (4, 7200, 16384, 32), (16, 16384, 6144, 64), (40, 7300, 1024, 128),
+                                            (20, 16500, 512, 64), (2, 40, 64000, 32), (2, 40, 64032, 32), (1, 33000, 256, 128)])
+@pytest.mark.parametrize("x8", [False, True])
+def test_q4_every_split(rows, n, k, group, x8):
+    """Sizes at which the tiles, the waves over k and what is held in LDS change."""
+    check_q4(rows, n, k, group, "bf16", x8)
 
 
 def test_q4_alignment_and_leading_axes():
