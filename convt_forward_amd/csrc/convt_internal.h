@@ -105,13 +105,6 @@ struct FastDiv {
     uint32_t m, s;
 };
 
-inline FastDiv fast_div_of(uint32_t d) {
-    uint32_t s = 0;
-    while (((uint64_t)1 << s) < d) ++s;
-    const uint64_t m = (((uint64_t)1 << 32) * (((uint64_t)1 << s) - d)) / d + 1;
-    return FastDiv{(uint32_t)m, s};
-}
-
 // All-phase GEMM (two-byte types; stride 2 and dilation 1 on the height and
 // width axes): a block computes every (height, width) residue of a q box for
 // 128 output channels and one depth residue, reading x in NC[D]HW and W in

@@ -10,6 +10,14 @@
 
 namespace convt {
 
+// The multiplier of fast_div for a divisor d >= 1 (see FastDiv).
+inline FastDiv divisor_of(uint32_t d) {
+    uint32_t s = 0;
+    while (((uint64_t)1 << s) < d) ++s;
+    const uint64_t m = (((uint64_t)1 << 32) * (((uint64_t)1 << s) - d)) / d + 1;
+    return FastDiv{(uint32_t)m, s};
+}
+
 // Most head dimensions a cache row may have: 64 lanes of 8 elements.
 constexpr int kMaxHeadDim = 512;
 

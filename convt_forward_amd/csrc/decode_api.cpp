@@ -87,8 +87,8 @@ convt_status cache_move(const convt_cache_desc *cache, const convt_cache_rows *r
     a.kv_heads = cache->kv_heads;
     a.page_size = cache->page_size;
     a.head_dim = cache->head_dim;
-    a.div_heads = convt::fast_div_of((uint32_t)cache->kv_heads);
-    a.div_page = convt::fast_div_of((uint32_t)cache->page_size);
+    a.div_heads = convt::divisor_of((uint32_t)cache->kv_heads);
+    a.div_page = convt::divisor_of((uint32_t)cache->page_size);
     if (write && a.n_slots == 0) return CONVT_OK;  // no slot is in the cache
     return device_status(convt::launch_cache(a, cache->dtype, cache->quantised, write, (hipStream_t)stream));
 }
@@ -272,8 +272,8 @@ convt_status convt_attend(const convt_attend_problem *problem, const void *q, co
     a.chunks = info.chunks;
     a.chunk_tokens = info.chunk_tokens;
     a.scale_log2e = (float)((double)p.scale * 1.4426950408889634074);
-    a.div_page = convt::fast_div_of((uint32_t)c.page_size);
-    a.div_heads = convt::fast_div_of((uint32_t)p.heads);
+    a.div_page = convt::divisor_of((uint32_t)c.page_size);
+    a.div_heads = convt::divisor_of((uint32_t)p.heads);
     const hipStream_t s = (hipStream_t)stream;
     const bool mfma = info.route == CONVT_ATTEND_MFMA && aligned(q, 16) && aligned(k_cache, 16) &&
                       aligned(v_cache, 16) && aligned(k_scale, 16) && aligned(v_scale, 16);

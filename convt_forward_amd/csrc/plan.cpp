@@ -328,6 +328,13 @@ int64_t nchw_halo(const DevParams &dp, int P, int T0, int T1, int T2) {
 }
 
 // ---- all-phase two-byte GEMM -------------------------------------------
+FastDiv fast_div_of(uint32_t d) {
+    uint32_t s = 0;
+    while (((uint64_t)1 << s) < d) ++s;
+    const uint64_t m = (((uint64_t)1 << 32) * (((uint64_t)1 << s) - d)) / d + 1;
+    return FastDiv{(uint32_t)m, s};
+}
+
 // Plan the all-phase kernel (k_gemm_allphase.hip) for a forward problem with
 // a two-byte element type, or return false if it does not apply: it needs
 // stride 2 and dilation 1 on the height and width axes with even kernel
