@@ -18,8 +18,10 @@ constexpr int kWaves = 4;
 // 64 tokens a wave and step. A lane first takes one token and the whole dot
 // product with q (held in LDS), then the lanes turn to the head dimension and
 // add the 64 values p[t] V[t], one token after the other. Simple and general;
-// its loads of K run along the lanes' own rows, which the caches gather, so
-// it stays well below the memory rate that the matrix-core kernel reaches.
+// its loads of K run along the lanes' own rows, which the caches gather, and each
+// query head reads its kv head again, so it stays well below the memory rate
+// that the matrix-core kernel reaches (4 streams of 100-131 K, bf16: 3.1 ms against
+// 0.33). It serves float32, odd head dimensions, pages and alignments.
 template <typename T, bool Q8>
 __global__ __launch_bounds__(64 * kWaves) void attend_direct(AttendArgs a) {
     typedef typename std::conditional<Q8, uint8_t, T>::type C;

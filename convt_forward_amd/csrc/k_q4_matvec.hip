@@ -20,7 +20,9 @@ constexpr int kRows = 8;  // rows of x a wave carries at once
 
 // A wave per output column n: each lane takes 8 consecutive k at a time, its
 // 8 weights in one word, and up to 8 rows of x against them. The group's
-// scale multiplies the lane's sum of 8 products, all in float32.
+// scale multiplies the lane's sum of 8 products, all in float32. Unpacking and
+// multiplying bound it (16 e4m3 rows x 8192 x 32768: 497 us against 34 on the
+// matrix cores); it serves float32 and what those do not take.
 template <typename T, bool X8>
 __global__ __launch_bounds__(256) void q4_direct(Q4Args a) {
     typedef typename std::conditional<X8, uint8_t, T>::type X;

@@ -10,7 +10,7 @@
 //   two-byte x: a weight w (0 .. 15) becomes the E value 16 + w by placing its
 //     bits into the mantissa of 16.0, a shift and an and-or for two weights;
 //     24 sum x is taken off. 16 + w keeps the sums within a factor of 6 of
-//     those for w - 8: 2^-21 of the result against the 2^-9 or 2^-12 of its
+//     those for w - 8: 2^-21 of the result against the 2^-8 or 2^-11 of its
 //     rounding.
 //   e4m3 x: the byte 0000wwww is the e4m3 value w * 2^-9, below and above the
 //     normal range alike, so 8 weights take a shift and two ands, x stays in
@@ -29,6 +29,11 @@
 //
 // Waves of a block share columns with different k (WK of them, joined through
 // LDS at the end) or take other columns (WN).
+//
+// Measured: 16 e4m3 rows x 8192 x 32768 (134 MB of weights): 33-36 us, 4 TB/s; its
+// weights' loads alone 25, the products add 1, x (read by every block through
+// the caches) the rest. One bf16 row: 32-34 us. One row x 4096 x 4096, 8.7 MB:
+// 4.7 us, of which 2.5 are an empty launch and 2.5 a bare read of 8 MB.
 #include "decode.h"
 #include "kdecode.h"
 
@@ -49,17 +54,6 @@ struct Q4Args {
 };
 
 constexpr int kMaxWaves = 8;
-
-template <typename E> struct Vec8;
-template <> struct Vec8<__bf16> { typedef bf16x8 type; };
-template <> struct Vec8<_Float16> { typedef f16x8 type; };
-
-__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-__device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-}
 
 // 8 weights as 16 + w, in the order (0, 4), (1, 5), (2, 6), (3, 7).
 template <typename E> __device__ __forceinline__ typename Vec8<E>::type unpack(uint32_t w) {

@@ -7,7 +7,12 @@
 // every output written once, which is what bounds the kernel (HBM). A row is
 // held by LANES threads in NV pieces of 8 elements each: a wave for short
 // rows (no barrier), a block of 256 for ordinary ones, of 1024 for long
-// ones; rows longer than that are read a second time (norm_wide).
+// ones; rows longer than that are read a second time (norm_wide). All of a
+// row's loads are in flight together, and 8 blocks a CU overlap one row's
+// reductions with another's loads.
+// Measured: 16384 rows x 8192, bf16 with residual to e4m3, 940 MB: 161 us, 5.8
+// TB/s, the rate of a bare read; 77 rows x 5001, f16: 4.0 us; one row x 1024:
+// 2.3 us, an empty launch.
 #include "decode.h"
 #include "kdecode.h"
 

@@ -32,6 +32,18 @@ template <> __device__ __forceinline__ void word_to_f32<_Float16>(uint32_t w, fl
 template <typename T> struct Arith { typedef T type; };
 template <> struct Arith<uint16_t> { typedef __bf16 type; };
 
+// 8 elements of an arithmetic type, an operand of the 16 x 16 x 32 products.
+template <typename E> struct Vec8;
+template <> struct Vec8<__bf16> { typedef bf16x8 type; };
+template <> struct Vec8<_Float16> { typedef f16x8 type; };
+
+__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
 // 8 elements in the registers they are loaded into.
 template <typename T> struct Raw8 { u32x4 w; };
 template <> struct Raw8<float> { f32x4 lo, hi; };
