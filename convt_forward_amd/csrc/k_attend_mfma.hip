@@ -45,14 +45,6 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kStep = 32;  // tokens a wave takes at a time
 
-// Two e4m3 codes (the low or high half of a word) as two E in a word, exact.
-template <typename E, bool HI> __device__ __forceinline__ uint32_t e4m3_pair(uint32_t w) {
-    if constexpr (__is_same(E, __bf16))
-        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
-    else
-        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
-}
-
 // Over the four lanes that share lane % 16.
 __device__ __forceinline__ float quad_max(float v) {
     auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);

@@ -3,18 +3,19 @@
 //
 // Reading the weights bounds it (HBM), and next to that unpacking them: at 8
 // TB/s a CU receives 26 weights a clock and has 64 vector lanes, so a weight
-// may cost about two lane operations. The products run on unsigned values that
-// cost less, with what they are too large by taken off as a multiple of sum x
-// of the group; that is one more product, of x with a constant, whose result is
-// where the group's sum starts. All products are exact in float32.
-//   two-byte x: a weight w (0 .. 15) becomes the E value 16 + w by placing its
-//     bits into the mantissa of 16.0, a shift and an and-or for two weights;
-//     24 sum x is taken off. 16 + w keeps the sums within a factor of 6 of
-//     those for w - 8: 2^-21 of the result against the 2^-8 or 2^-11 of its
-//     rounding.
-//   e4m3 x: the byte 0000wwww is the e4m3 value w * 2^-9, below and above the
-//     normal range alike, so 8 weights take a shift and two ands, x stays in
-//     8 bits, and 8 * 2^-9 sum x is taken off; the scale carries 2^9.
+// may cost about two lane operations. The byte 0000wwww is the e4m3 value
+// w * 2^-9, below and above that type's normal range alike, so a shift and two
+// ands make the bytes of 8 weights and four conversions (with the scale 2^9)
+// the E values w, 7 operations in all, exactly. (Placing the bits into the
+// mantissa of 16.0 takes 8, for 16 + w: 37 against 34 us for the case below.)
+// The 8 that w is too large by is taken off as 8 sum x of the group: one more
+// product, of x with a constant, whose result is where the group's sum
+// starts. All products are exact in float32, and w in place of w - 8 keeps
+// the sums within a factor of 2. e4m3 rows are widened to E, exactly, for
+// the same products: those on 8-bit operands would take the weights' bytes
+// as they are, but they line their terms up with fewer bits than float32
+// has (off by up to 6e-6 of the terms' magnitudes at k = 128, where these stay
+// below 6e-9).
 // One product serves up to 16 rows of x, and a group's scale multiplies its
 // finished sum, once for 4 results.
 //
@@ -23,17 +24,17 @@
 // the four lanes of an n hold 128 k; each product wants its 32 k from four
 // lanes, 8 each, so the words are transposed among the four lanes (4 lane
 // swaps for 4 words) and every group of 32 k or more stays in one product.
-// With e4m3 x and groups of 128 the product of 128 k takes the lanes' own 32 k.
-// Unpacking leaves a word's weights in another order, to which x is brought by
-// byte permutations; the sum does not mind.
+// (e4m3 x with groups of 128 takes the lanes' own 32 k of both instead.)
+// Unpacking leaves the even k of a word before the odd ones, and x is brought
+// to that order; the sum does not mind.
 //
 // Waves of a block share columns with different k (WK of them, joined through
 // LDS at the end) or take other columns (WN).
 //
-// Measured: 16 e4m3 rows x 8192 x 32768 (134 MB of weights): 33-36 us, 4 TB/s; its
-// weights' loads alone 25, the products add 1, x (read by every block through
-// the caches) the rest. One bf16 row: 32-34 us. One row x 4096 x 4096, 8.7 MB:
-// 4.7 us, of which 2.5 are an empty launch and 2.5 a bare read of 8 MB.
+// Measured: 16 e4m3 rows x 8192 x 32768 (134 MB of weights): 34 us, 4.1 TB/s; its
+// weights' loads alone take 25, x (read by every block through the caches)
+// most of the rest. One bf16 row: 31 us. One row x 4096 x 4096, 8.7 MB: 4.6
+// us, of which 2.5 are an empty launch and 2.5 a bare read of 8 MB.
 #include "decode.h"
 #include "kdecode.h"
 
@@ -55,39 +56,22 @@ struct Q4Args {
 
 constexpr int kMaxWaves = 8;
 
-// 8 weights as 16 + w, in the order (0, 4), (1, 5), (2, 6), (3, 7).
+// 8 weights, as they are, in the order (0, 2), (4, 6), (1, 3), (5, 7).
 template <typename E> __device__ __forceinline__ typename Vec8<E>::type unpack(uint32_t w) {
-    u32x4 v;
-    if constexpr (__is_same(E, __bf16)) {  // 7 mantissa bits: a weight at bits 3 .. 6
-        v = u32x4{w << 3, w >> 1, w >> 5, w >> 9};
-        for (int i = 0; i < 4; ++i) v[i] = (v[i] & 0x00780078u) | 0x41804180u;
-    } else {  // 10 mantissa bits: bits 6 .. 9
-        v = u32x4{w << 6, w << 2, w >> 2, w >> 6};
-        for (int i = 0; i < 4; ++i) v[i] = (v[i] & 0x03c003c0u) | 0x4c004c00u;
-    }
-    return __builtin_bit_cast(typename Vec8<E>::type, v);
+    const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
+    return __builtin_bit_cast(typename Vec8<E>::type, u32x4{e4m3_pair<E, false>(even, 512.0f), e4m3_pair<E, true>(even, 512.0f),
+                                                           e4m3_pair<E, false>(odd, 512.0f), e4m3_pair<E, true>(odd, 512.0f)});
 }
 
 // 8 consecutive x in the same order.
 template <typename E> __device__ __forceinline__ typename Vec8<E>::type order_x(u32x4 w) {
-    return __builtin_bit_cast(typename Vec8<E>::type, u32x4{lo_pair(w[0], w[2]), hi_pair(w[0], w[2]),
-                                                           lo_pair(w[1], w[3]), hi_pair(w[1], w[3])});
+    return __builtin_bit_cast(typename Vec8<E>::type, u32x4{lo_pair(w[0], w[1]), lo_pair(w[2], w[3]),
+                                                           hi_pair(w[0], w[1]), hi_pair(w[2], w[3])});
 }
-
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-
-__device__ __forceinline__ f32x4 mfma_e4m3(u32x2 a, u32x2 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(__builtin_bit_cast(long, a), __builtin_bit_cast(long, b), c, 0, 0, 0);
-}
-// both operands e4m3 (formats 0), unscaled
-__device__ __forceinline__ f32x4 mfma_e4m3(i32x8 a, i32x8 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
-}
-// 8 weights as e4m3 w * 2^-9, in the order 0, 2, 4, 6, 1, 3, 5, 7; 8 consecutive
-// codes of x in that order.
-__device__ __forceinline__ u32x2 unpack_e4m3(uint32_t w) { return u32x2{w & 0x0f0f0f0fu, (w >> 4) & 0x0f0f0f0fu}; }
-__device__ __forceinline__ u32x2 order_e4m3(uint32_t lo, uint32_t hi) {
-    return u32x2{__builtin_amdgcn_perm(hi, lo, 0x06040200u), __builtin_amdgcn_perm(hi, lo, 0x07050301u)};
+template <typename E> __device__ __forceinline__ typename Vec8<E>::type order_x(u32x2 w) {
+    const uint32_t even = __builtin_amdgcn_perm(w[1], w[0], 0x06040200u), odd = __builtin_amdgcn_perm(w[1], w[0], 0x07050301u);
+    return __builtin_bit_cast(typename Vec8<E>::type, u32x4{e4m3_pair<E, false>(even), e4m3_pair<E, true>(even),
+                                                           e4m3_pair<E, false>(odd), e4m3_pair<E, true>(odd)});
 }
 
 // Word j of lane group g <-> word g of lane group j (groups of 16 lanes).
@@ -104,12 +88,13 @@ __device__ __forceinline__ u32x4 transpose_groups(u32x4 w) {
 template <typename E, bool X8, int GS, int NT, int MT, int U, bool XL>
 __global__ __launch_bounds__(64 * kMaxWaves) void q4_mfma(Q4Args a) {
     typedef typename Vec8<E>::type E8;
-    constexpr bool WIDE = X8 && GS == 128;  // products of 128 k
-    // x of a chunk: 4 pieces of 8 k for the products of 32 k, or 32 k in two
-    typedef typename std::conditional<X8 && !WIDE, u32x2, u32x4>::type XW;
-    constexpr int NX = WIDE ? 2 : 4;
     constexpr int XS = X8 ? 1 : 2;
-    constexpr int XLANE = WIDE ? 32 : 8, XSTEP = WIDE ? 16 : 32;  // k between lane groups, between pieces
+    // x of a chunk in 16-byte pieces of a lane: 8 k each for the products of 32 k, or, of
+    // e4m3 rows, the lane's own 32 k, as W has them
+    constexpr int NX = X8 ? 2 : 4, XLANE = X8 ? 32 : 8, XSTEP = X8 ? 16 : 32;
+    // Where a product may mix the chunk's 32 k of each lane group (one group of
+    // weights), e4m3 x and W stay in the lanes they were loaded into.
+    constexpr bool STAY = X8 && GS == 128;
     constexpr int G = 128 / GS;  // groups of a chunk
     constexpr int GU = G * U;    // groups of a stage
     // The block's scales, a row of scale_row for each of its columns, and x with
@@ -140,7 +125,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void q4_mfma(Q4Args a) {
 
     struct Stage {
         u32x4 w[U][NT];
-        XW x[XL ? 1 : U][MT][NX];
+        u32x4 x[XL ? 1 : U][MT][NX];
     };
     const char *xl = (const char *)lds + a.x_at;  // with XL: the lane's place in x
     {
@@ -162,7 +147,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void q4_mfma(Q4Args a) {
                 for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int j = 0; j < NX; ++j)
-                        st.x[u][mt][j] = *(const XW *)(xp[mt] + ((c * U + u) * 128 + j * XSTEP) * XS);
+                        st.x[u][mt][j] = *(const u32x4 *)(xp[mt] + ((c * U + u) * 128 + j * XSTEP) * XS);
     };
     auto load_part = [&](Stage &st, int c) {
 #pragma unroll
@@ -178,8 +163,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void q4_mfma(Q4Args a) {
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int j = 0; j < NX; ++j) {
-                        st.x[u][mt][j] = XW{};
-                        if (k0 + (WIDE ? 0 : j * 32) < a.k) st.x[u][mt][j] = *(const XW *)(xp[mt] + (k0 + j * XSTEP) * XS);
+                        st.x[u][mt][j] = u32x4{0, 0, 0, 0};
+                        if (k0 + (X8 ? g : j) * 32 < a.k)
+                            st.x[u][mt][j] = *(const u32x4 *)(xp[mt] + (k0 + j * XSTEP) * XS);
                     }
         }
     };
@@ -189,92 +175,60 @@ __global__ __launch_bounds__(64 * kMaxWaves) void q4_mfma(Q4Args a) {
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) acc[t][mt] = f32x4{0, 0, 0, 0};
-    // -24 of E, twice in a word; -8 * 2^-9 of e4m3, four times
-    const uint32_t less = X8 ? 0x88888888u : __is_same(E, __bf16) ? 0xc1c0c1c0u : 0xce00ce00u;
+    const uint32_t less2 = __is_same(E, __bf16) ? 0xc100c100u : 0xc800c800u;  // -8 of E, twice
+    const E8 less = __builtin_bit_cast(E8, u32x4{less2, less2, less2, less2});
 
     const uint16_t *srow = (const uint16_t *)lds + (wn * NT * 16 + r) * a.scale_row;
     auto scale_of = [&](int t, int group) { return half_to_f32<E>(srow[t * 16 * a.scale_row + group]); };
     auto x_of = [&](const Stage &st, int c, int u, int mt, int j) {
-        if constexpr (XL) return *(const XW *)(xl + ((c * U + u) * 128 + j * XSTEP) * XS);
+        if constexpr (XL) return *(const u32x4 *)(xl + ((c * U + u) * 128 + j * XSTEP) * XS);
         else return st.x[u][mt][j];
     };
     auto chunk = [&](const Stage &st, int c, int u) {
-        if constexpr (WIDE) {
-            i32x8 xf[MT], off;
-            f32x4 sx[MT];
+        u32x4 w[NT];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) off[i] = (int)less;
+        for (int t = 0; t < NT; ++t) w[t] = STAY ? st.w[u][t] : transpose_groups(st.w[u][t]);
+        // e4m3 x: the words of the four products, low and high
+        u32x4 xlo[MT], xhi[MT];
+        if constexpr (X8) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const XW x = x_of(st, c, u, mt, j);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const u32x2 v = order_e4m3(x[2 * i], x[2 * i + 1]);
-                        xf[mt][4 * j + 2 * i] = (int)v[0];
-                        xf[mt][4 * j + 2 * i + 1] = (int)v[1];
-                    }
+                const u32x4 p = x_of(st, c, u, mt, 0), q = x_of(st, c, u, mt, 1);
+                xlo[mt] = u32x4{p[0], p[2], q[0], q[2]};
+                xhi[mt] = u32x4{p[1], p[3], q[1], q[3]};
+                if constexpr (!STAY) {
+                    xlo[mt] = transpose_groups(xlo[mt]);
+                    xhi[mt] = transpose_groups(xhi[mt]);
                 }
-                sx[mt] = mfma_e4m3(xf[mt], off, f32x4{0, 0, 0, 0});
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            constexpr int J = GS / 32;  // products of a group
+            E8 xf[MT][J];
+            f32x4 sx[MT];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                sx[mt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    if constexpr (X8) xf[mt][j] = order_x<E>(u32x2{xlo[mt][i * J + j], xhi[mt][i * J + j]});
+                    else xf[mt][j] = order_x<E>(x_of(st, c, u, mt, i * J + j));
+                    sx[mt] = mfma16(xf[mt][j], less, sx[mt]);
+                }
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                i32x8 wf;
+                const float s = scale_of(t, c * GU + u * G + i);
+                E8 wf[J];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const u32x2 v = unpack_e4m3(st.w[u][t][i]);
-                    wf[2 * i] = (int)v[0];
-                    wf[2 * i + 1] = (int)v[1];
-                }
-                const float s = scale_of(t, c * GU + u) * 512.0f;
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) acc[t][mt] += s * mfma_e4m3(xf[mt], wf, sx[mt]);
-            }
-        } else {
-            u32x4 w[NT];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) w[t] = transpose_groups(st.w[u][t]);
-#pragma unroll
-            for (int i = 0; i < G; ++i) {
-                constexpr int J = GS / 32;  // products of a group
-                typedef typename std::conditional<X8, u32x2, E8>::type F;
-                F xf[MT][J];
-                f32x4 sx[MT];
+                for (int j = 0; j < J; ++j) wf[j] = unpack<E>(w[t][i * J + j]);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    sx[mt] = f32x4{0, 0, 0, 0};
+                    f32x4 sum = sx[mt];
 #pragma unroll
-                    for (int j = 0; j < J; ++j) {
-                        const XW x = x_of(st, c, u, mt, i * J + j);
-                        if constexpr (X8) {
-                            xf[mt][j] = order_e4m3(x[0], x[1]);
-                            sx[mt] = mfma_e4m3(xf[mt][j], u32x2{less, less}, sx[mt]);
-                        } else {
-                            xf[mt][j] = order_x<E>(x);
-                            sx[mt] = mfma16(xf[mt][j], __builtin_bit_cast(E8, u32x4{less, less, less, less}), sx[mt]);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const float s = scale_of(t, c * GU + u * G + i) * (X8 ? 512.0f : 1.0f);
-                    F wf[J];
-#pragma unroll
-                    for (int j = 0; j < J; ++j) {
-                        if constexpr (X8) wf[j] = unpack_e4m3(w[t][i * J + j]);
-                        else wf[j] = unpack<E>(w[t][i * J + j]);
-                    }
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        f32x4 sum = sx[mt];
-#pragma unroll
-                        for (int j = 0; j < J; ++j) {
-                            if constexpr (X8) sum = mfma_e4m3(xf[mt][j], wf[j], sum);
-                            else sum = mfma16(xf[mt][j], wf[j], sum);
-                        }
-                        acc[t][mt] += s * sum;
-                    }
+                    for (int j = 0; j < J; ++j) sum = mfma16(xf[mt][j], wf[j], sum);
+                    acc[t][mt] += s * sum;
                 }
             }
         }
@@ -412,9 +366,9 @@ template <typename E, bool X8, int GS, int NT, int MT> void go(Q4Args a, int wk,
 // Waves and tiles. Few columns: one tile a block and 8 waves over k, for as
 // many blocks as there are CUs. Many columns: each block reads all of x, which
 // costs as much as the weights when x is 16 rows (16 x 8192 e4m3 rows x
-// 32768 columns: 33 us with 4 tiles a wave, 37 with 2, 42 with 1), so waves
+// 32768 columns: 34 us with 4 tiles a wave, some 4 more with 2, 9 with 1), so waves
 // take more tiles. x that fits in LDS is cheap to share (1 x 8192 bf16 x
-// 32768: 31 us from LDS with 2 tiles and 2 x 4 waves, 34 from the caches).
+// 32768: 3 us less from LDS, with 2 tiles and 2 x 4 waves, than from the caches).
 // The scales of a block's columns fit in 64 KB of LDS: fewer tiles otherwise.
 template <typename E, bool X8, int GS> void run(const Q4Args &a, hipStream_t s) {
     const int tiles = (a.n + 15) / 16;

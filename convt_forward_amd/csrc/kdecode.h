@@ -44,6 +44,15 @@ __device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
+// Two e4m3 codes (the low or high half of a word) as two E in a word, times a
+// power of two, exact.
+template <typename E, bool HI> __device__ __forceinline__ uint32_t e4m3_pair(uint32_t w, float scale = 1.0f) {
+    if constexpr (__is_same(E, __bf16))
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, HI));
+    else
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, scale, HI));
+}
+
 // 8 elements in the registers they are loaded into.
 template <typename T> struct Raw8 { u32x4 w; };
 template <> struct Raw8<float> { f32x4 lo, hi; };

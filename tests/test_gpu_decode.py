@@ -501,6 +501,30 @@ def test_q4_large(rows):
     check_q4(rows, 300, 4096, 32, "bf16", True, strided=True)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("x8", [False, True])
+def test_q4_small_terms_beside_a_large_one(dt, group, x8):
+    """A channel 448 times the others whose weights stand for 0: sums in float32 keep the others, sums that
+    line up their terms with fewer bits would not."""
+    t, n, k = TYPES[dt], 64, 256
+    g = torch.Generator().manual_seed(7)
+    x = torch.rand(4, k, generator=g).to(E4M3).float() + 2.0 ** -4
+    x = x.to(E4M3)
+    x[:, 5] = 448.0
+    w = torch.randint(0, 256, (n, k // 2), generator=g, dtype=torch.uint8)
+    w[:, 2] = (w[:, 2] & 15) | 0x80  # k = 5: the high bits of byte 2
+    scales = torch.full((n, k // group), 0.5).to(t)
+    xs = torch.ones(4)
+    got = C.q4_matvec(x.to(DEV) if x8 else x.to(t).to(DEV), w.to(DEV), scales.to(DEV), x_scale=xs.to(DEV) if x8 else None)
+    wf = torch.stack([w & 15, w >> 4], -1).reshape(n, k).double() - 8
+    assert (wf[:, 5] == 0).all()
+    want = x.double() @ wf.t() * 0.5
+    # terms of at most 15 |x|, some k / 32 + 8 roundings of their sums
+    mag = x.double().abs().sum(-1, keepdim=True) * 15 * 0.5
+    within(got, want, rounding(t, want) * (1 + 2.0 ** -6) + mag * (k / 32 + 8) * U, "y")
+
+
 @pytest.mark.parametrize("rows,n,k,group", [(1, 16400, 12288, 32), (4, 7200, 16384, 32), (16, 16384, 6144, 64), (40, 7300, 1024, 128),
                                             (20, 16500, 512, 64), (2, 40, 64000, 32), (2, 40, 64032, 32), (1, 33000, 256, 128)])
 @pytest.mark.parametrize("x8", [False, True])
