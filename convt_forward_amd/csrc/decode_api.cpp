@@ -139,6 +139,11 @@ convt_status attend_check(const convt_attend_problem *p, convt_attend_info *info
     int64_t chunk = p->max_length / 128 * items / slots;  // steps of 128 tokens
     chunk = chunk < 16 ? (chunk + 1) * 128 : 2048;
     if (chunk > longest) chunk = (longest + 127) / 128 * 128;
+    // What one block reads in about the time of the second launch stays one
+    // part: 512 tokens of two kv heads, e4m3, 7.2 us in one launch, 7.4 in two
+    // (8.0 and 12.3 called from Python); 32 streams of 512 x 8 heads 9.4 and 13.5.
+    const int64_t single = c.head_dim <= 128 ? 512 : 256;
+    if (p->max_length <= single) chunk = single;
     int64_t chunks = ceil_div(p->max_length, chunk);
     if (chunks < 1) chunks = 1;
     // the grid's second axis holds the parts
