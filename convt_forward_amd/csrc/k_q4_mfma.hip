@@ -54,7 +54,7 @@ struct Q4Args {
     int32_t x_at, x_row;         // LDS with XL: byte offset of x, bytes of a row of it
 };
 
-constexpr int kMaxWaves = 8;
+constexpr int kMaxWaves = 8;  // of a block; 4 with 64 rows of x, for their registers
 
 // 8 weights, as they are, in the order (0, 2), (4, 6), (1, 3), (5, 7).
 template <typename E> __device__ __forceinline__ typename Vec8<E>::type unpack(uint32_t w) {
@@ -86,7 +86,7 @@ __device__ __forceinline__ u32x4 transpose_groups(u32x4 w) {
 // NT: tiles of 16 columns a wave, MT: tiles of 16 rows of x, U: chunks of 128 k a
 // stage, XL: x is held in LDS.
 template <typename E, bool X8, int GS, int NT, int MT, int U, bool XL>
-__global__ __launch_bounds__(64 * kMaxWaves) void q4_mfma(Q4Args a) {
+__global__ __launch_bounds__(64 * (MT == 4 ? 4 : kMaxWaves)) void q4_mfma(Q4Args a) {
     typedef typename Vec8<E>::type E8;
     constexpr int XS = X8 ? 1 : 2;
     // x of a chunk in 16-byte pieces of a lane: 8 k each for the products of 32 k, or, of
@@ -376,7 +376,7 @@ template <typename E, bool X8, int GS> void run(const Q4Args &a, hipStream_t s) 
     const bool four = wide * 4 <= 65536, two = wide * 2 <= 65536;
     if (a.rows > 32) {
         if (tiles >= 448 && two) go<E, X8, GS, 2, 4>(a, 4, 1, s);
-        else go<E, X8, GS, 1, 4>(a, 8, 1, s);
+        else go<E, X8, GS, 1, 4>(a, 4, 1, s);
     } else if (a.rows > 16) {
         if (tiles >= 1024 && four) go<E, X8, GS, 4, 2>(a, 4, 1, s);
         else if (tiles >= 448 && two) go<E, X8, GS, 2, 2>(a, 4, 1, s);

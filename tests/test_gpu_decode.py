@@ -469,7 +469,7 @@ def check_q4(rows, n, k, group, dt, x8, route="auto", seed=0, strided=False):
     wf = (torch.stack([w & 15, w >> 4], -1).reshape(n, k).double() - 8) * scales.double().repeat_interleave(group, 1)
     xf = x.double() * (1 if xs is None else xs.double().unsqueeze(-1))
     want = xf @ wf.t()
-    # the matrix cores see w + 16 (at most 31) and take 24 times the sum of x off again
+    # the sums run on w, or on w plus an offset, with the excess of sum x taken off: terms below 32 |x|
     mag = xf.abs() @ scales.double().repeat_interleave(group, 1).t() * 32
     within(got, want, rounding(t, want) * (1 + 2.0 ** -6) + mag * (k / 64 + 64) * U, "y")
     if y is not None:
