@@ -331,7 +331,7 @@ __global__ __launch_bounds__(64 * (MT == 4 ? 4 : kMaxWaves)) void q4_mfma(Q4Args
 }
 
 // Most LDS that x may take of a block (XL).
-constexpr size_t kXLds = 32768;
+constexpr size_t kXLds = 40960;
 
 template <typename E, bool X8, int GS, int NT, int MT> void go(Q4Args a, int wk, int wn, hipStream_t s) {
     // 128 bytes of each column a stage (a whole line) where the registers allow
@@ -367,7 +367,9 @@ template <typename E, bool X8, int GS, int NT, int MT> void go(Q4Args a, int wk,
 // many blocks as there are CUs. Many columns: each block reads all of x, which
 // costs as much as the weights when x is 16 rows (16 x 8192 e4m3 rows x
 // 32768 columns: 34 us with 4 tiles a wave, some 4 more with 2, 9 with 1), so waves
-// take more tiles. x that fits in LDS is cheap to share (1 x 8192 bf16 x
+// take more tiles, from the number of columns on that still leaves blocks for most
+// CUs (16 x 8192 bf16 rows x 12000 columns: 20 us with 4 tiles, 26 with 2; x 8192
+// columns: 19 with 4, 15 with 2). x that fits in LDS is cheap to share (1 x 8192 bf16 x
 // 32768: 3 us less from LDS, with 2 tiles and 2 x 4 waves, than from the caches).
 // The scales of a block's columns fit in 64 KB of LDS: fewer tiles otherwise.
 template <typename E, bool X8, int GS> void run(const Q4Args &a, hipStream_t s) {
@@ -381,11 +383,11 @@ template <typename E, bool X8, int GS> void run(const Q4Args &a, hipStream_t s) 
         if (tiles >= 1024 && four) go<E, X8, GS, 4, 2>(a, 4, 1, s);
         else if (tiles >= 448 && two) go<E, X8, GS, 2, 2>(a, 4, 1, s);
         else go<E, X8, GS, 1, 2>(a, 8, 1, s);
-    } else if ((size_t)a.rows * a.k * (X8 ? 1 : 2) <= kXLds - 16 * 512 && wide * 4 <= 32768) {
+    } else if ((size_t)a.rows * ((a.k + 256) * (X8 ? 1 : 2) + 64) <= kXLds && wide * 4 <= 32768) {
         if (tiles >= 1024) go<E, X8, GS, 2, 1>(a, 4, 2, s);
         else go<E, X8, GS, 1, 1>(a, 8, 1, s);
     } else {
-        if (tiles >= 1024 && four) go<E, X8, GS, 4, 1>(a, tiles >= 2048 ? 4 : 8, 1, s);
+        if (tiles >= 700 && four) go<E, X8, GS, 4, 1>(a, tiles >= 2048 ? 4 : 8, 1, s);
         else if (tiles >= 448 && two) go<E, X8, GS, 2, 1>(a, 8, 1, s);
         else go<E, X8, GS, 1, 1>(a, 8, 1, s);
     }
