@@ -148,9 +148,8 @@ __global__ __launch_bounds__(256) void attend_join(AttendArgs a, int lanes_log2)
     const int h = (int)(blockIdx.x - b * (uint32_t)a.heads);
     int len = a.lengths[b];
     len = len < 0 ? 0 : len > a.max_length ? a.max_length : len;
-    // part 0 is there even for an empty stream
-    int n = (len + a.chunk_tokens - 1) / a.chunk_tokens;
-    if (n < 1) n = 1;
+    // part 0 is there even for an empty stream (len + chunk_tokens may pass 31 bits)
+    const int n = len > 0 ? (len - 1) / a.chunk_tokens + 1 : 1;
     const int D = a.head_dim;
     const int64_t part0 = (int64_t)blockIdx.x * a.chunks;
     const float *ml = a.part_ml + part0 * 2;

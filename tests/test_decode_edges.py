@@ -1,0 +1,30 @@
+"""CPU tests of the decoding-step operators at the edges of what they accept: the split of the
+longest lengths, and the Python binding's checks, none of which needs a device."""
+import ctypes
+
+import pytest
+import torch
+
+import convt_forward_amd as C
+from convt_forward_amd import decode as D
+
+
+def attend_query(max_length, batch=1, heads=1, kv_heads=1, page=2 ** 20, dim=16, table_width=2048, table_stride=2048):
+    strides = (ctypes.c_int64 * 3)(kv_heads * page * dim, page * dim, dim)
+    cache = D.CacheDesc(1, strides, strides, kv_heads, page, dim, 1, 0, 0)
+    two = (ctypes.c_int64 * 2)(heads * dim, dim)
+    p = D.AttendProblem(cache, max_length, two, two, table_width, table_stride, batch, heads, 0, 1.0)
+    info = D.AttendInfo()
+    return D.lib().convt_attend_query(ctypes.byref(p), ctypes.byref(info)), info
+
+
+@pytest.mark.parametrize("batch", [1, 40, 3000])
+@pytest.mark.parametrize("length", [2 ** 30 + 1, 2 ** 31 - 2 ** 16, 2 ** 31 - 2 ** 16 + 1, 2 ** 31 - 4097])
+def test_parts_of_the_longest_lengths(length, batch):
+    """Up to the longest length accepted the parts cover it, and the first token of every part is
+    an index of 31 bits; one more is refused."""
+    st, i = attend_query(length, batch)
+    assert st == 0 and 1 <= i.chunks <= 32768
+    assert i.chunks == (length - 1) // i.chunk_tokens + 1
+    assert (i.chunks - 1) * i.chunk_tokens < 2 ** 31
+    assert attend_query(2 ** 31 - 4096, batch)[0] == 1

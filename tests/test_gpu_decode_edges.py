@@ -1,0 +1,46 @@
+"""GPU tests of the decoding-step operators at the edges of what they accept: the longest lengths,
+weights far below the largest, infinite values, rows that repeat in memory. Plain forms and
+bounds are those of tests/decode_util.py."""
+import math
+
+import pytest
+import torch
+
+import convt_forward_amd as C
+from tests.decode_util import TYPES, U, attend64, attend_bound, within
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+def rand(*shape, seed=0):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed + sum(shape)))
+
+
+def one_stream(k, v, page=16):
+    """A cache of one stream in scattered pages, its table and length; k and v [kv heads, tokens, dims]."""
+    heads, n, dim = k.shape
+    width = -(-n // page)
+    cache = C.KVCache.new(width + 2, heads, page, dim, dtype=k.dtype)
+    table = torch.randperm(width + 2, generator=torch.Generator().manual_seed(n))[:width].to(torch.int32).view(1, width).to(DEV)
+    at = torch.arange(n, device=DEV)
+    C.cache_write(cache, k.transpose(0, 1).contiguous().to(DEV), v.transpose(0, 1).contiguous().to(DEV),
+                  C.cache_slots(table, torch.zeros_like(at), at, page))
+    return cache, table, torch.tensor([n], dtype=torch.int32, device=DEV)
+
+
+def test_attend_at_the_longest_length():
+    """2^31 - 4097 tokens, the most a call takes, from one page that the table repeats. Every weight is the
+    same, and 2^16 tokens of a page have the value 1, the others 0: all parts have to be joined."""
+    page, ones, length = 2 ** 20, 2 ** 16, 2 ** 31 - 4097
+    k = torch.zeros(1, 1, page, 16, device=DEV).bfloat16()
+    v = torch.zeros_like(k)
+    v[:, :, :ones] = 1
+    table = torch.zeros(1, 2048, dtype=torch.int32, device=DEV)
+    out, lse = C.decode_attention(torch.ones(1, 1, 16, device=DEV).bfloat16(), C.KVCache(k, v), table,
+                                  torch.tensor([length], dtype=torch.int32, device=DEV), max_length=length, lse=True)
+    # 2048 * 2^16 tokens of value 1; sums of whole numbers, 32768 parts joined, one rounding to bfloat16
+    want = 2048 * ones / length
+    assert ((out.double() - want).abs() <= want * (2.0 ** -8 + 2.0 ** -12)).all(), out
+    assert abs(lse.item() - math.log(length)) <= 32 * 2.0 ** -20
