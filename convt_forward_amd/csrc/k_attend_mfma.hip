@@ -23,10 +23,13 @@
 //
 // Roundings: Q and K enter as stored (e4m3 codes are exact in bf16 and f16;
 // their scales multiply the float32 scores). p (times the value's scale) is
-// rounded to float16 where V is float16, 2^-11 of its value. Where V is
-// bfloat16 or e4m3 it goes in as the sum of two bfloat16 values (2^-16),
-// since one bfloat16 (2^-8) would be as coarse as the output itself; the
-// second product costs nothing beside the loads.
+// rounded to float16 where V is float16: 2^-11 of its value. For that it carries
+// a factor 2^15 (p <= 1, so 2^15 p fits, and float16's steps are relative from
+// 2^-14 on), which the waves' join takes off: weights down to 2^-29 of the
+// wave's largest keep their 11 bits, and smaller ones are off by at most 2^-40
+// of it. Where V is bfloat16 or e4m3, p goes in as the sum of two bfloat16
+// values (2^-16), since one bfloat16 (2^-8) would be as coarse as the output
+// itself; the second product costs nothing beside the loads.
 //
 // Measured (kernel alone, then with the join): 4 streams of 100-131 K tokens, 8 kv
 // heads of 128, bf16, 1.89 GB: 327, 333 us, 5.8 TB/s; 32 ragged streams up to
@@ -73,6 +76,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 4 : DP == 128 ? 3 : 1) void
     typedef typename Vec8<E>::type E8;
     typedef typename Vec8<EV>::type EV8;
     constexpr bool SPLIT = __is_same(EV, __bf16);
+    constexpr float RAISE = SPLIT ? 1.0f : 0x1p15f;  // the factor that p and o carry
     constexpr int CS = Q8 ? 1 : 2;        // bytes of a cache element
     constexpr int NC = DP / 32;           // products of 32 dims for a score tile
     constexpr int KL = Q8 ? DP / 64 : NC; // 16-byte loads of a lane for a score tile
@@ -271,7 +275,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 4 : DP == 128 ? 3 : 1) void
             for (int i = 0; i < 4; ++i) {
                 const float e = __builtin_amdgcn_exp2f(s[u][i] - base);
                 l += e;
-                p[u * 4 + i] = Q8 ? e * vscale[u][i] : e;
+                p[u * 4 + i] = Q8 ? e * vscale[u][i] : e * RAISE;
             }
         u32x4 ph, pl;
 #pragma unroll
@@ -338,6 +342,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 4 : DP == 128 ? 3 : 1) void
         for (int d = lane; d < D; d += 64) {
             float v = 0.0f;
             for (int w = 0; w < kWaves; ++w) v += o_lds[w][h * LD + d] * f[w];
+            v *= 1.0f / RAISE;
             if (a.chunks > 1)
                 a.part_o[part * D + d] = v;
             else

@@ -44,3 +44,20 @@ def test_attend_at_the_longest_length():
     want = 2048 * ones / length
     assert ((out.double() - want).abs() <= want * (2.0 ** -8 + 2.0 ** -12)).all(), out
     assert abs(lse.item() - math.log(length)) <= 32 * 2.0 ** -20
+
+
+@pytest.mark.parametrize("others", [1, 15, 100, 700])
+@pytest.mark.parametrize("bits", [10, 14, 17, 20, 23, 24.7, 25.3, 28])
+def test_attend_weights_far_below_the_largest(bits, others):
+    """One token (of value 0) takes nearly all the weight; the others, each 2^-bits of it, carry the result."""
+    D, t = 64, torch.float16
+    q = torch.ones(1, 1, D, dtype=t)
+    k, v = torch.zeros(1, 1, others + 1, D, dtype=t), 512 + 64 * rand(1, 1, others + 1, D).clamp(-3, 3)
+    v = v.to(t)
+    k[0, 0, 0], v[0, 0, 0] = bits * math.log(2) / D, 0
+    cache, table, lens = one_stream(k[0], v[0])
+    out = C.decode_attention(q.to(DEV), cache, table, lens, scale=1.0, route="mfma")
+    want, _, mag, top = attend64(q, k.double(), v.double(), [others + 1], 1.0)
+    # a weight is off by 2^-11 of itself, or by half of float16's smallest step where the largest is 2^15
+    bound = attend_bound(want, mag, top, D, others + 1, t, 2.0 ** -11) + (others + 1) * 2.0 ** -40 * v.double().abs().max()
+    within(out, want, bound, f"{others} weights of 2^-{bits}")
