@@ -29,7 +29,9 @@
 // wave's largest keep their 11 bits, and smaller ones are off by at most 2^-40
 // of it. Where V is bfloat16 or e4m3, p goes in as the sum of two bfloat16
 // values (2^-16), since one bfloat16 (2^-8) would be as coarse as the output
-// itself; the second product costs nothing beside the loads.
+// itself; the second product costs nothing beside the loads. Its V has the
+// largest finite value where V is infinite: the low part may be 0 or negative,
+// and the first product carries the infinity.
 //
 // Measured (kernel alone, then with the join): 4 streams of 100-131 K tokens, 8 kv
 // heads of 128, bf16, 1.89 GB: 327, 333 us, 5.8 TB/s; 32 ragged streams up to
@@ -60,6 +62,17 @@ __device__ __forceinline__ float quad_sum(float v) {
     v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
     auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// Two bfloat16 values with infinities (and NaN) replaced by the largest finite
+// value of their sign, as integers: unsigned, that bounds the negative ones;
+// signed, the positive ones.
+__device__ __forceinline__ uint32_t finite_bf16(uint32_t w) {
+    typedef uint16_t u2 __attribute__((ext_vector_type(2)));
+    typedef int16_t i2 __attribute__((ext_vector_type(2)));
+    const u2 n = __builtin_elementwise_min(__builtin_bit_cast(u2, w), u2{0xff7f, 0xff7f});
+    const i2 v = __builtin_elementwise_min(__builtin_bit_cast(i2, n), i2{0x7f7f, 0x7f7f});
+    return __builtin_bit_cast(uint32_t, v);
 }
 
 template <int BYTES> struct Piece;
@@ -302,11 +315,17 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 4 : DP == 128 ? 3 : 1) void
                     w[t] = vr[t][jw * 4 / VP][jw % (VP / 4)];
                 }
             }
-            const u32x4 lo = {lo_pair(w[0], w[1]), lo_pair(w[2], w[3]), lo_pair(w[4], w[5]), lo_pair(w[6], w[7])};
-            const u32x4 hi = {hi_pair(w[0], w[1]), hi_pair(w[2], w[3]), hi_pair(w[4], w[5]), hi_pair(w[6], w[7])};
+            u32x4 lo = {lo_pair(w[0], w[1]), lo_pair(w[2], w[3]), lo_pair(w[4], w[5]), lo_pair(w[6], w[7])};
+            u32x4 hi = {hi_pair(w[0], w[1]), hi_pair(w[2], w[3]), hi_pair(w[4], w[5]), hi_pair(w[6], w[7])};
             o[2 * jw] = mfma16(__builtin_bit_cast(EV8, lo), __builtin_bit_cast(EV8, ph), o[2 * jw]);
             o[2 * jw + 1] = mfma16(__builtin_bit_cast(EV8, hi), __builtin_bit_cast(EV8, ph), o[2 * jw + 1]);
             if constexpr (SPLIT) {
+                if constexpr (!Q8)  // e4m3 has no infinities
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        lo[i] = finite_bf16(lo[i]);
+                        hi[i] = finite_bf16(hi[i]);
+                    }
                 o[2 * jw] = mfma16(__builtin_bit_cast(EV8, lo), __builtin_bit_cast(EV8, pl), o[2 * jw]);
                 o[2 * jw + 1] = mfma16(__builtin_bit_cast(EV8, hi), __builtin_bit_cast(EV8, pl), o[2 * jw + 1]);
             }

@@ -125,7 +125,10 @@ convt_status convt_cache_read(const convt_cache_desc *cache, const convt_cache_r
  * sees nothing (length <= 0) gets out = 0 and lse = -infinity. Lengths above
  * max_length are cut to it; tokens of a page id outside 0 .. n_pages - 1 are
  * left out. Nothing past a stream's length is read into the result, whatever
- * it holds.
+ * it holds. An infinite or NaN value that is seen makes its dim of the result
+ * so, as the formula does; a weight too small to be held (2^-126 of the
+ * largest, 2^-40 over a float16 cache on the matrix cores) times an infinite
+ * value is NaN.
  *
  * max_length bounds the lengths the call handles: at most table_width *
  * page_size, and below 2^31 - 4096. The length axis is cut into chunks that are computed by different

@@ -61,3 +61,26 @@ def test_attend_weights_far_below_the_largest(bits, others):
     # a weight is off by 2^-11 of itself, or by half of float16's smallest step where the largest is 2^15
     bound = attend_bound(want, mag, top, D, others + 1, t, 2.0 ** -11) + (others + 1) * 2.0 ** -40 * v.double().abs().max()
     within(out, want, bound, f"{others} weights of 2^-{bits}")
+
+
+@pytest.mark.parametrize("route", ["auto", "direct"])
+@pytest.mark.parametrize("dt", sorted(TYPES))
+@pytest.mark.parametrize("n", [5, 100, 700])
+def test_attend_infinite_values(dt, route, n):
+    """An infinite value that is seen makes its dim of the result infinite, two of both signs make it NaN, a
+    NaN NaN; all others stay as they are, and values past the length are not seen."""
+    t, D = TYPES[dt], 64
+    q, k, v = rand(1, 2, D, seed=1).to(t), (0.3 * rand(1, 1, n + 3, D, seed=2)).to(t), rand(1, 1, n + 3, D, seed=3).to(t)
+    v[0, 0, 1, 3] = math.inf
+    v[0, 0, n - 1, 17] = -math.inf
+    v[0, 0, 0, 40], v[0, 0, n - 2, 40] = math.inf, -math.inf
+    v[0, 0, n // 2, 50] = math.nan
+    v[0, 0, 2, 60], v[0, 0, 3, 60] = torch.finfo(t).max / 8, -torch.finfo(t).max / 8
+    v[0, 0, n:] = math.inf
+    cache, table, _ = one_stream(k[0], v[0])
+    out = C.decode_attention(q.to(DEV), cache, table, torch.tensor([n], dtype=torch.int32, device=DEV), scale=D ** -0.5,
+                             route=route).cpu()
+    want, _, mag, top = attend64(q, k.double(), v.double(), [n], D ** -0.5)
+    assert (want[0, :, 3] == math.inf).all() and (want[0, :, 17] == -math.inf).all() and want[0, :, [40, 50]].isnan().all()
+    p_step = 2.0 ** -11 if dt == "f16" else 2.0 ** -15
+    within(out, want, attend_bound(want, mag, top, D, n, t, p_step), f"{dt} {route} {n}")
