@@ -130,6 +130,8 @@ def _rows(t, name: str) -> Tuple[int, int]:
         raise ValueError(f"the last axis of {name} must be contiguous")
     if len(shape) == 2:
         return shape[0], stride[0]
+    if 0 in shape[:-1]:
+        return 0, width
     rows, step = 1, 0
     for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
         if n == 1:

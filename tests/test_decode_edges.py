@@ -28,3 +28,9 @@ def test_parts_of_the_longest_lengths(length, batch):
     assert i.chunks == (length - 1) // i.chunk_tokens + 1
     assert (i.chunks - 1) * i.chunk_tokens < 2 ** 31
     assert attend_query(2 ** 31 - 4096, batch)[0] == 1
+
+
+@pytest.mark.parametrize("shape", [(2, 0, 8), (0, 2, 8), (3, 0, 4, 8), (2, 3, 0, 8), (0, 0, 8), (0, 8)])
+def test_no_rows_in_any_axis(shape):
+    assert D._rows(torch.zeros(shape), "t")[0] == 0
+    assert D._rows(torch.zeros(shape)[..., 2:5], "t")[0] == 0
