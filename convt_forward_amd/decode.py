@@ -154,6 +154,15 @@ def _empty(shape, dtype, device):
     return torch.empty_strided(shape, stride[::-1], dtype=dtype, device=device)
 
 
+def _check_workspace(t, need: int, device) -> None:
+    """need bytes from t's first element on are t's own (an expanded tensor has fewer than it counts)."""
+    _check(t, "workspace", device=device)
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if t.numel() * t.element_size() < need:
+        raise ValueError("workspace too small")
+
+
 def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -395,6 +404,7 @@ def decode_attention(q, cache: KVCache, page_table, lengths, scale: Optional[flo
     heads / kv_heads query heads share a kv head. scale is 1 / sqrt(head_dim)
     by default. max_length bounds the lengths (default: what the table can
     hold); a close bound saves launching blocks for parts no stream reaches.
+    A given workspace is contiguous, with at least attend_plan's workspace_bytes.
     Returns out [batch, heads, head_dim]; with lse (True, or a float32 tensor
     [batch, heads] to fill) the pair (out, lse), lse the logarithm of the sum
     of exponentials. A stream that sees nothing gets zeros and -infinity."""
@@ -425,8 +435,8 @@ def decode_attention(q, cache: KVCache, page_table, lengths, scale: Optional[flo
         if info.workspace_bytes:
             workspace = _empty((info.workspace_bytes,), torch.uint8, cache.device)
             owned.append(workspace)
-    elif not workspace.is_cuda or workspace.numel() * workspace.element_size() < info.workspace_bytes:
-        raise ValueError("workspace too small")
+    else:
+        _check_workspace(workspace, info.workspace_bytes, cache.device)
     st = (_ready or lib()).convt_attend(ctypes.byref(p), q.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(), _ptr(cache.k_scale),
           _ptr(cache.v_scale), page_table.data_ptr(), lengths.data_ptr(), out.data_ptr(), _ptr(lse_t),
           _ptr(workspace), sh)

@@ -34,3 +34,15 @@ def test_parts_of_the_longest_lengths(length, batch):
 def test_no_rows_in_any_axis(shape):
     assert D._rows(torch.zeros(shape), "t")[0] == 0
     assert D._rows(torch.zeros(shape)[..., 2:5], "t")[0] == 0
+
+
+def test_workspace_is_the_callers_whole_memory():
+    """A workspace whose elements lie in less memory than they count, or on another device, is refused."""
+    here = torch.device("cpu")
+    D._check_workspace(torch.empty(64, dtype=torch.uint8), 64, here)
+    D._check_workspace(torch.empty(200, dtype=torch.uint8)[100:], 64, here)
+    D._check_workspace(torch.empty(4, 4), 64, here)
+    for bad, why in [(torch.empty(1, dtype=torch.uint8).expand(64), "contiguous"), (torch.empty(128, dtype=torch.uint8)[::2], "contiguous"),
+                     (torch.empty(63, dtype=torch.uint8), "too small"), (torch.empty(64, dtype=torch.uint8, device="meta"), "is on meta")]:
+        with pytest.raises(ValueError, match=why):
+            D._check_workspace(bad, 64, here)

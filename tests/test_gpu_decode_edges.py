@@ -84,3 +84,17 @@ def test_attend_infinite_values(dt, route, n):
     assert (want[0, :, 3] == math.inf).all() and (want[0, :, 17] == -math.inf).all() and want[0, :, [40, 50]].isnan().all()
     p_step = 2.0 ** -11 if dt == "f16" else 2.0 ** -15
     within(out, want, attend_bound(want, mag, top, D, n, t, p_step), f"{dt} {route} {n}")
+
+
+def test_attend_refuses_a_workspace_it_would_write_past():
+    cache, table, lens = one_stream(rand(2, 700, 64).bfloat16(), rand(2, 700, 64, seed=1).bfloat16())
+    q = rand(1, 4, 64).bfloat16().to(DEV)
+    need = C.attend_plan(cache, q, table)[1].workspace_bytes
+    assert need > 0
+    for bad in (torch.empty(1, dtype=torch.uint8, device=DEV).expand(need), torch.empty(2 * need, dtype=torch.uint8, device=DEV)[::2],
+                torch.empty(need, dtype=torch.uint8), torch.empty(need - 1, dtype=torch.uint8, device=DEV)):
+        with pytest.raises(ValueError, match="workspace"):
+            C.decode_attention(q, cache, table, lens, workspace=bad)
+    torch.cuda.synchronize()
+    out = C.decode_attention(q, cache, table, lens, workspace=torch.empty(need, dtype=torch.uint8, device=DEV))
+    assert torch.equal(out, C.decode_attention(q, cache, table, lens))
