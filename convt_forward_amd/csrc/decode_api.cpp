@@ -36,6 +36,12 @@ bool strides_ok(const int64_t *s, int n, int64_t least = 1) {
     return true;
 }
 
+// Spacing of `width` elements' rows: at least the width, or, where they are
+// only read, 0 (one row for all).
+bool row_stride_ok(int64_t s, int64_t width, bool read) {
+    return (s >= width && s <= kMaxStride) || (read && s == 0);
+}
+
 convt_status check_cache(const convt_cache_desc &c) {
     const convt_status st = check_dtype(c.dtype);
     if (st != CONVT_OK) return st;
@@ -113,8 +119,7 @@ convt_status attend_check(const convt_attend_problem *p, convt_attend_info *info
     if (p->batch < 0 || p->heads < 1 || p->heads % c.kv_heads != 0) return CONVT_ERR_INVALID_ARGUMENT;
     if ((int64_t)p->batch * p->heads > kMaxBlocks) return CONVT_ERR_UNSUPPORTED;
     if (p->table_width < 0 || p->table_width > kMaxIndex) return CONVT_ERR_INVALID_ARGUMENT;
-    if (p->batch > 1 && (p->table_stride < p->table_width || p->table_stride > kMaxStride))
-        return CONVT_ERR_INVALID_ARGUMENT;
+    if (p->batch > 1 && !row_stride_ok(p->table_stride, p->table_width, true)) return CONVT_ERR_INVALID_ARGUMENT;
     if (p->max_length < 0 || p->max_length > kMaxIndex - 4096 || p->max_length > p->table_width * c.page_size)
         return CONVT_ERR_INVALID_ARGUMENT;
     if (!strides_ok(p->q_stride, 2, 0) || !strides_ok(p->out_stride, 2)) return CONVT_ERR_INVALID_ARGUMENT;
@@ -176,7 +181,7 @@ convt_status q4_check(const convt_q4_problem *p, int32_t *route) {
     if (p->rows < 0 || p->n < 0 || p->k < 0 || p->rows > kMaxIndex || p->n > kMaxIndex || p->k > kMaxIndex)
         return CONVT_ERR_INVALID_ARGUMENT;
     if (p->group < 8 || p->group % 8 != 0 || p->k % p->group != 0) return CONVT_ERR_INVALID_ARGUMENT;
-    if (p->rows > 1 && (p->x_stride < p->k || p->y_stride < p->n || p->x_stride > kMaxStride || p->y_stride > kMaxStride))
+    if (p->rows > 1 && (!row_stride_ok(p->x_stride, p->k, true) || !row_stride_ok(p->y_stride, p->n, false)))
         return CONVT_ERR_INVALID_ARGUMENT;
     if (p->route < CONVT_Q4_AUTO || p->route > CONVT_Q4_MFMA) return CONVT_ERR_INVALID_ARGUMENT;
     if ((p->n + 3) / 4 > kMaxBlocks) return CONVT_ERR_UNSUPPORTED;
@@ -200,10 +205,11 @@ convt_status convt_rms_norm(const convt_rms_norm_problem *problem, const void *x
     if (!(p.eps >= 0.0f) || !isfinite(p.eps)) return CONVT_ERR_INVALID_ARGUMENT;
     if (p.rows < 0 || p.rows > kMaxIndex || p.width < 1 || p.width > ((int64_t)1 << 24)) return CONVT_ERR_INVALID_ARGUMENT;
     if (p.rows > 1) {
-        const int64_t strides[4] = {p.x_stride, p.y_stride, p.has_residual ? p.residual_stride : p.width,
-                                    p.has_residual ? p.residual_out_stride : p.width};
-        for (int64_t s : strides)
-            if (s < p.width || s > kMaxStride) return CONVT_ERR_INVALID_ARGUMENT;
+        if (!row_stride_ok(p.x_stride, p.width, true) || !row_stride_ok(p.y_stride, p.width, false))
+            return CONVT_ERR_INVALID_ARGUMENT;
+        if (p.has_residual && (!row_stride_ok(p.residual_stride, p.width, true) ||
+                               !row_stride_ok(p.residual_out_stride, p.width, false)))
+            return CONVT_ERR_INVALID_ARGUMENT;
     }
     if (p.has_residual ? 0 : (residual || residual_out)) return CONVT_ERR_INVALID_ARGUMENT;
     if (!p.quantise && scale) return CONVT_ERR_INVALID_ARGUMENT;

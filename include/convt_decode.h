@@ -49,8 +49,8 @@ extern "C" {
  * (the norm itself uses h before that rounding). y is rounded to the element
  * type, or, with quantise = 1, quantised per row: y then holds e4m3 codes
  * (bytes) and scale one float32 per row.
- * rows >= 0, width in 1 .. 2^24; row strides >= width (read only when rows >
- * 1). residual and residual_out are required iff has_residual; scale iff
+ * rows >= 0, width in 1 .. 2^24; row strides >= width, those of x and residual
+ * also 0 (read only when rows > 1). residual and residual_out are required iff has_residual; scale iff
  * quantise. residual_out may be residual or x itself, and y may be x or
  * residual when not quantised and the strides agree (each element is read
  * before its place is written); otherwise outputs overlap no input.
@@ -137,7 +137,7 @@ convt_status convt_cache_read(const convt_cache_desc *cache, const convt_cache_r
  *
  * heads is a multiple of cache.kv_heads, batch * heads below 2^24; q and out have the given batch and
  * head strides (the last is 1), page_table int32 [batch][table_width] with
- * table_stride between its rows, lengths int32 [batch]. scale is finite.
+ * table_stride (0, or at least table_width) between its rows, lengths int32 [batch]. scale is finite.
  * Routes: ATTEND_MFMA (two-byte types, head_dim a multiple of 16 and at most
  * 256, page_size a multiple of 16, 16-byte aligned cache rows) on the matrix
  * cores; ATTEND_DIRECT for everything else. route = CONVT_ATTEND_AUTO picks;
@@ -190,7 +190,7 @@ convt_status convt_attend(const convt_attend_problem *problem, const void *q, co
  * x_scale is left out otherwise). y is [rows][n] of the element type. Sums in
  * float32, one rounding.
  * rows >= 0, n >= 0, k >= 0; group a multiple of 8 that divides k; row
- * strides of x >= k and of y >= n (read only when rows > 1); rows and k below
+ * strides of x >= k or 0 and of y >= n (read only when rows > 1); rows and k below
  * 2^31, n at most 2^26 - 4.
  * Routes: Q4_MFMA (two-byte types, group 32, 64 or 128, w and x rows 16-byte
  * aligned) on the matrix cores; Q4_DIRECT for everything

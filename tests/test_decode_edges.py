@@ -46,3 +46,12 @@ def test_workspace_is_the_callers_whole_memory():
                      (torch.empty(63, dtype=torch.uint8), "too small"), (torch.empty(64, dtype=torch.uint8, device="meta"), "is on meta")]:
         with pytest.raises(ValueError, match=why):
             D._check_workspace(bad, 64, here)
+
+
+def test_rows_that_are_only_read_may_repeat():
+    """A stride of 0 is taken for x and page tables, and refused for what is written."""
+    route = ctypes.c_int32()
+    for xs, ys, want in ((0, 5, 0), (64, 5, 0), (0, 0, 1), (1, 5, 1), (-1, 5, 1)):
+        p = D.Q4Problem(3, 5, 64, 32, xs, ys, 1, 0, 0, 0)
+        assert D.lib().convt_q4_query(ctypes.byref(p), ctypes.byref(route)) == want, (xs, ys)
+    assert [attend_query(100, batch=2, table_stride=s)[0] for s in (0, 2048, 1, 2047, -1)] == [0, 0, 1, 1, 1]

@@ -98,3 +98,32 @@ def test_attend_refuses_a_workspace_it_would_write_past():
     torch.cuda.synchronize()
     out = C.decode_attention(q, cache, table, lens, workspace=torch.empty(need, dtype=torch.uint8, device=DEV))
     assert torch.equal(out, C.decode_attention(q, cache, table, lens))
+
+
+@pytest.mark.parametrize("quantise", [False, True])
+def test_norm_of_repeated_rows(quantise):
+    """x and residual that are one row in memory for all rows (stride 0)."""
+    x, r = rand(1, 200).bfloat16().to(DEV), rand(1, 200, seed=1).bfloat16().to(DEV)
+    w = torch.ones(200, device=DEV).bfloat16()
+    want = C.rms_norm(x.repeat(5, 1), w, residual=r.repeat(5, 1), quantise=quantise)
+    got = C.rms_norm(x.expand(5, 200), w, residual=r.expand(5, 200), quantise=quantise)
+    for a, b in zip(got, want):
+        assert (a is None and b is None) or torch.equal(a.float(), b.float())
+
+
+@pytest.mark.parametrize("route", ["auto", "direct"])
+def test_q4_of_repeated_rows(route):
+    w, s = (t.to(DEV) for t in C.q4_quantise(rand(50, 256).bfloat16(), 64))
+    x = rand(1, 256, seed=2).bfloat16().to(DEV)
+    for rows in (2, 20, 70):
+        assert torch.equal(C.q4_matvec(x.expand(rows, 256), w, s, route=route), C.q4_matvec(x.repeat(rows, 1), w, s, route=route))
+
+
+@pytest.mark.parametrize("route", ["auto", "direct"])
+def test_attend_over_one_table_for_all_streams(route):
+    n, D = 700, 64
+    cache, table, _ = one_stream(rand(2, n, D).bfloat16(), rand(2, n, D, seed=1).bfloat16())
+    q = rand(3, 4, D).bfloat16().to(DEV)
+    lens = torch.tensor([n, 0, 33], dtype=torch.int32, device=DEV)
+    got = C.decode_attention(q, cache, table.expand(3, table.shape[1]), lens, route=route)
+    assert torch.equal(got, C.decode_attention(q, cache, table.repeat(3, 1), lens, route=route))
