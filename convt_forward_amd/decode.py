@@ -232,31 +232,40 @@ class KVCache:
     strides whose last is 1 (a [page, token, head, dim] cache is passed as its permuted view). With
     k_scale and v_scale (contiguous float32 [n_pages, kv_heads, page_size]) k and v
     hold e4m3 codes (torch.float8_e4m3fn); else they hold the element type. The tensors stay the
-    caller's; slot s of a page table stands for page s // page_size, token s % page_size."""
+    caller's; one of the same shape may be put in another's place (cache.k = ...), the other
+    attributes follow from them. Slot s of a page table stands for page s // page_size, token s % page_size."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         if k.dim() != 4:
             raise ValueError("k must be [n_pages, kv_heads, page_size, head_dim]")
         if (k_scale is None) != (v_scale is None):
             raise ValueError("k_scale and v_scale go together")
-        self.quantised = k_scale is not None
-        if not self.quantised:
+        quantised = k_scale is not None
+        if not quantised:
             _code(k, "k")
-        _check(k, "k", None, _E4M3 if self.quantised else None)
+        _check(k, "k", None, _E4M3 if quantised else None)
         _check(v, "v", k.shape, k.dtype, k.device)
-        self.n_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        n_pages, kv_heads, page_size, head_dim = k.shape
         for t, name in ((k, "k"), (v, "v")):
-            if self.head_dim > 1 and t.stride(3) != 1:
+            if head_dim > 1 and t.stride(3) != 1:
                 raise ValueError(f"the last axis of {name} must be contiguous")
-        if self.quantised:
+        if quantised:
             for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
                 _check(t, name, k.shape[:3], torch.float32, k.device)
                 if not t.is_contiguous():
                     raise ValueError(f"{name} must be contiguous")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.device = k.device
-        self._descs: Dict[torch.dtype, CacheDesc] = {}
-        self._attends: Dict[tuple, tuple] = {}
+        # descriptions and plans of calls, which hold the tensors' strides
+        descs: Dict[torch.dtype, CacheDesc] = {}
+        attends: Dict[tuple, tuple] = {}
+        self.__dict__.update(k=k, v=v, k_scale=k_scale, v_scale=v_scale, quantised=quantised, n_pages=n_pages, kv_heads=kv_heads,
+                             page_size=page_size, head_dim=head_dim, device=k.device, _descs=descs, _attends=attends)
+
+    def __setattr__(self, name, value):
+        if name not in ("k", "v", "k_scale", "v_scale"):
+            raise AttributeError(f"{name} of a KVCache cannot be assigned")
+        tensors = dict(k=self.k, v=self.v, k_scale=self.k_scale, v_scale=self.v_scale)
+        tensors[name] = value
+        self.__init__(**tensors)
 
     @classmethod
     def new(cls, n_pages: int, kv_heads: int, page_size: int, head_dim: int, dtype=torch.bfloat16, quantised=False,

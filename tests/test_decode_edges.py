@@ -55,3 +55,33 @@ def test_rows_that_are_only_read_may_repeat():
         p = D.Q4Problem(3, 5, 64, 32, xs, ys, 1, 0, 0, 0)
         assert D.lib().convt_q4_query(ctypes.byref(p), ctypes.byref(route)) == want, (xs, ys)
     assert [attend_query(100, batch=2, table_stride=s)[0] for s in (0, 2048, 1, 2047, -1)] == [0, 0, 1, 1, 1]
+
+
+def fake_cache(monkeypatch, *shape, quantised=False):
+    """A KVCache whose tensors lie on the CPU; only calls that launch nothing are made of it."""
+    monkeypatch.setattr(D, "_check", lambda *a, **k: None)
+    scales = [torch.zeros(shape[:3]) for _ in range(2)] if quantised else [None, None]
+    kind = D._E4M3 if quantised else torch.bfloat16
+    return C.KVCache(*(torch.zeros(shape, dtype=torch.uint8).to(kind) for _ in range(2)), *scales)
+
+
+@pytest.mark.parametrize("quantised", [False, True])
+def test_cache_follows_its_tensors(monkeypatch, quantised):
+    """A tensor put in the place of another is checked like the first, and calls see its strides."""
+    cache = fake_cache(monkeypatch, 4, 2, 16, 64, quantised=quantised)
+    assert list(cache._desc(torch.bfloat16, "k").k_stride) == [2048, 1024, 64]
+    q, table = torch.zeros(3, 4, 64).bfloat16(), torch.zeros(3, 4, dtype=torch.int32)
+    assert list(C.attend_plan(cache, q, table)[0].cache.k_stride) == [2048, 1024, 64]
+    other = torch.zeros(4, 16, 2, 64, dtype=torch.uint8).to(cache.k.dtype).transpose(1, 2)
+    cache.k = other
+    assert cache.k is other and list(cache._desc(torch.bfloat16, "k").k_stride) == [2048, 64, 128]
+    assert list(cache._desc(torch.bfloat16, "k").v_stride) == [2048, 1024, 64]
+    assert list(C.attend_plan(cache, q, table)[0].cache.k_stride) == [2048, 64, 128]
+    with pytest.raises(ValueError):
+        cache.v = other.permute(0, 1, 3, 2)  # its last axis is not contiguous
+    with pytest.raises(ValueError):
+        cache.k_scale = None if quantised else torch.zeros(4, 2, 16)
+    for name in ("quantised", "n_pages", "kv_heads", "page_size", "head_dim", "device", "other"):
+        with pytest.raises(AttributeError, match="KVCache"):
+            setattr(cache, name, 1)
+    assert cache.k is other and cache.quantised == quantised
