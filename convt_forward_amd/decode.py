@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 from typing import Dict, Optional, Tuple
 
 import torch
@@ -369,6 +370,11 @@ def attend_plan(cache: KVCache, q, page_table, scale=None, max_length: Optional[
                 route: str = "auto") -> Tuple[AttendProblem, AttendInfo]:
     """The problem and the route, parts and workspace size of a decode_attention call
     on these tensors (kept with the cache for calls of the same shapes)."""
+    # plain numbers: a tensor in the key would stand for itself, not for its value
+    if scale is not None:
+        scale = float(scale)
+    if max_length is not None:
+        max_length = operator.index(max_length)
     out_stride = None if out is None else out.stride()
     key = (q.dtype, q.shape, q.stride(), page_table.shape, page_table.stride(), scale, max_length, out_stride, route)
     got = cache._attends.get(key)

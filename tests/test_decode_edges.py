@@ -85,3 +85,16 @@ def test_cache_follows_its_tensors(monkeypatch, quantised):
         with pytest.raises(AttributeError, match="KVCache"):
             setattr(cache, name, 1)
     assert cache.k is other and cache.quantised == quantised
+
+
+def test_plan_goes_by_the_value_of_its_arguments(monkeypatch):
+    """A scale or length given as a tensor counts with the value it has at the call."""
+    cache = fake_cache(monkeypatch, 4, 2, 16, 64)
+    q, table = torch.zeros(3, 4, 64).bfloat16(), torch.zeros(3, 4, dtype=torch.int32)
+    scale, most = torch.tensor(0.5), torch.tensor(40)
+    assert (lambda p: (p.scale, p.max_length))(C.attend_plan(cache, q, table, scale, most)[0]) == (0.5, 40)
+    scale.fill_(0.25), most.fill_(50)
+    assert (lambda p: (p.scale, p.max_length))(C.attend_plan(cache, q, table, scale, most)[0]) == (0.25, 50)
+    assert C.attend_plan(cache, q, table, 0.25, 50)[0].max_length == 50
+    with pytest.raises(TypeError):
+        C.attend_plan(cache, q, table, 0.25, 50.0)
