@@ -374,8 +374,8 @@ class Plan:
             owned.append(workspace)
         elif workspace.numel() * workspace.element_size() < self.workspace_bytes:
             raise ValueError("workspace too small")
-        self.forward_ptr(x.data_ptr(), w.data_ptr(), bias.data_ptr() if bias is not None else 0,
-                         y.data_ptr(), workspace.data_ptr(), sh)
+        _on_device(x.device, self.forward_ptr, x.data_ptr(), w.data_ptr(),
+                   bias.data_ptr() if bias is not None else 0, y.data_ptr(), workspace.data_ptr(), sh)
         _tie_to_stream(owned, ext)
         return y
 
@@ -410,8 +410,8 @@ class Plan:
             owned.append(workspace)
         elif workspace.numel() * workspace.element_size() < self.bwd_workspace_bytes:
             raise ValueError("workspace too small")
-        self.backward_data_ptr(dy.data_ptr(), w.data_ptr(), dx.data_ptr(), workspace.data_ptr(),
-                               sh)
+        _on_device(dy.device, self.backward_data_ptr, dy.data_ptr(), w.data_ptr(), dx.data_ptr(),
+                   workspace.data_ptr(), sh)
         _tie_to_stream(owned, ext)
         return dx
 
@@ -431,6 +431,24 @@ def _launch_stream(stream, device):
     if obj.cuda_stream == torch.cuda.current_stream(device).cuda_stream:
         return obj.cuda_stream, None
     return obj.cuda_stream, obj
+
+
+_one_device = None  # whether there is only one GPU
+
+
+def _on_device(device, call, *args):
+    """call(*args) with `device` current: a launch goes to the current device, whatever
+    tensors it names (the default stream's handle is 0 on every device)."""
+    global _one_device
+    if _one_device:
+        return call(*args)
+    import torch
+    if _one_device is None:
+        _one_device = torch.cuda.device_count() == 1
+    if torch.cuda.current_device() == device.index:
+        return call(*args)
+    with torch.cuda.device(device):
+        return call(*args)
 
 
 def _tie_to_stream(tensors, ext) -> None:

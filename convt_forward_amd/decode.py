@@ -22,7 +22,7 @@ from typing import Dict, Optional, Tuple
 
 import torch
 
-from . import ConvtError, DTYPES, _launch_stream as _given_stream, _tie_to_stream
+from . import ConvtError, DTYPES, _launch_stream as _given_stream, _on_device, _tie_to_stream
 from . import lib as _load
 
 ATTEND_ROUTES = {"auto": 0, "direct": 1, "mfma": 2}
@@ -219,8 +219,8 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, quantise: bool = False
     elif scale is not None:
         raise ValueError("scale without quantise")
     p = NormProblem(rows, width, xs, rs, ys, ros, code, 0 if residual is None else 1, 1 if quantise else 0, eps)
-    st = (_ready or lib()).convt_rms_norm(ctypes.byref(p), x.data_ptr(), weight.data_ptr(), _ptr(residual), y.data_ptr(), _ptr(scale),
-          _ptr(residual_out), sh)
+    st = _on_device(device, (_ready or lib()).convt_rms_norm, ctypes.byref(p), x.data_ptr(), weight.data_ptr(),
+                    _ptr(residual), y.data_ptr(), _ptr(scale), _ptr(residual_out), sh)
     if st:
         _raise(st, "convt_rms_norm")
     if ext is not None:
@@ -323,8 +323,9 @@ def cache_write(cache: KVCache, k, v, slots, stream=None) -> KVCache:
     rows = _cache_rows(cache, k, v, slots)
     d = cache._desc(k.dtype, "k")
     sh, _ = _launch_stream(stream, cache.device)
-    st = (_ready or lib()).convt_cache_write(ctypes.byref(d), ctypes.byref(rows), k.data_ptr(), v.data_ptr(), slots.data_ptr(),
-          cache.k.data_ptr(), cache.v.data_ptr(), _ptr(cache.k_scale), _ptr(cache.v_scale), sh)
+    st = _on_device(cache.device, (_ready or lib()).convt_cache_write, ctypes.byref(d), ctypes.byref(rows), k.data_ptr(),
+                    v.data_ptr(), slots.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(), _ptr(cache.k_scale),
+                    _ptr(cache.v_scale), sh)
     if st:
         _raise(st, "convt_cache_write")
     return cache
@@ -351,8 +352,9 @@ def cache_read(cache: KVCache, slots, dtype=None, k=None, v=None, stream=None):
     if k.dtype != dtype:
         raise ValueError(f"k must be {dtype}")
     rows = _cache_rows(cache, k, v, slots)
-    st = (_ready or lib()).convt_cache_read(ctypes.byref(d), ctypes.byref(rows), cache.k.data_ptr(), cache.v.data_ptr(),
-          _ptr(cache.k_scale), _ptr(cache.v_scale), slots.data_ptr(), k.data_ptr(), v.data_ptr(), sh)
+    st = _on_device(cache.device, (_ready or lib()).convt_cache_read, ctypes.byref(d), ctypes.byref(rows),
+                    cache.k.data_ptr(), cache.v.data_ptr(), _ptr(cache.k_scale), _ptr(cache.v_scale), slots.data_ptr(),
+                    k.data_ptr(), v.data_ptr(), sh)
     if st:
         _raise(st, "convt_cache_read")
     if ext is not None:
@@ -452,9 +454,9 @@ def decode_attention(q, cache: KVCache, page_table, lengths, scale: Optional[flo
             owned.append(workspace)
     else:
         _check_workspace(workspace, info.workspace_bytes, cache.device)
-    st = (_ready or lib()).convt_attend(ctypes.byref(p), q.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(), _ptr(cache.k_scale),
-          _ptr(cache.v_scale), page_table.data_ptr(), lengths.data_ptr(), out.data_ptr(), _ptr(lse_t),
-          _ptr(workspace), sh)
+    st = _on_device(cache.device, (_ready or lib()).convt_attend, ctypes.byref(p), q.data_ptr(), cache.k.data_ptr(),
+                    cache.v.data_ptr(), _ptr(cache.k_scale), _ptr(cache.v_scale), page_table.data_ptr(), lengths.data_ptr(),
+                    out.data_ptr(), _ptr(lse_t), _ptr(workspace), sh)
     if st:
         _raise(st, "convt_attend")
     if ext is not None:
@@ -517,8 +519,8 @@ def q4_matvec(x, w, scales, x_scale=None, y=None, stream=None, route: str = "aut
         _check(y, "y", shape, dtype, device)
         ys = _rows(y, "y")[1]
     p = Q4Problem(rows, n, k, k // groups if groups else 8, xs, ys, code, 1 if quantised else 0, Q4_ROUTES[route], 0)
-    st = (_ready or lib()).convt_q4_matvec(ctypes.byref(p), x.data_ptr(), _ptr(x_scale), w.data_ptr(), scales.data_ptr(),
-          y.data_ptr(), sh)
+    st = _on_device(device, (_ready or lib()).convt_q4_matvec, ctypes.byref(p), x.data_ptr(), _ptr(x_scale), w.data_ptr(),
+                    scales.data_ptr(), y.data_ptr(), sh)
     if st:
         _raise(st, "convt_q4_matvec")
     if ext is not None:

@@ -98,3 +98,69 @@ def test_plan_goes_by_the_value_of_its_arguments(monkeypatch):
     assert C.attend_plan(cache, q, table, 0.25, 50)[0].max_length == 50
     with pytest.raises(TypeError):
         C.attend_plan(cache, q, table, 0.25, 50.0)
+
+
+class Elsewhere:
+    """A stand-in for a tensor of a second GPU: everything but its device is the CPU tensor's."""
+
+    def __init__(self, t):
+        self.t, self.device, self.is_cuda = t, torch.device("cuda", 1), True
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+class FakeDevices:
+    """Keeps the current device, and the one that was current at each call of the library."""
+
+    def __init__(self):
+        self.now, self.calls = 0, []
+
+    def __getattr__(self, name):
+        return lambda *args: self.calls.append((name, self.now)) or 0
+
+
+@pytest.fixture
+def two_devices(monkeypatch):
+    fake = FakeDevices()
+
+    class Context:
+        def __init__(self, device):
+            self.index = torch.device(device).index
+
+        def __enter__(self):
+            self.before, fake.now = fake.now, self.index
+
+        def __exit__(self, *a):
+            fake.now = self.before
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: fake.now)
+    monkeypatch.setattr(torch.cuda, "device", Context)
+    monkeypatch.setattr(C, "_one_device", False)
+    for module in (C, D):
+        monkeypatch.setattr(module, "_launch_stream", lambda stream, device: (0, None))
+    monkeypatch.setattr(D, "_empty", lambda shape, dtype, device: Elsewhere(torch.empty(tuple(shape), dtype=dtype)))
+    return fake
+
+
+def test_calls_go_to_their_tensors_device(two_devices, monkeypatch):
+    """With device 0 current, calls on tensors of device 1 are launched there, and leave device 0 current."""
+    C.lib(), D.lib()
+    monkeypatch.setattr(D, "_ready", two_devices)
+    t = lambda *shape, dtype=torch.bfloat16: Elsewhere(torch.zeros(*shape, dtype=dtype))  # noqa: E731
+    cache = C.KVCache(t(4, 2, 16, 64), t(4, 2, 16, 64))
+    C.rms_norm(t(3, 64), t(64))
+    C.cache_write(cache, t(3, 2, 64), t(3, 2, 64), t(3, dtype=torch.int64))
+    C.cache_read(cache, t(3, dtype=torch.int64))
+    C.decode_attention(t(1, 4, 64), cache, t(1, 4, dtype=torch.int32), t(1, dtype=torch.int32))
+    C.q4_matvec(t(3, 64), t(5, 32, dtype=torch.uint8), t(5, 2))
+    assert [c for c in two_devices.calls if c[0] != "convt_attend_query"] == [
+        (f"convt_{n}", 1) for n in ("rms_norm", "cache_write", "cache_read", "attend", "q4_matvec")]
+    plan = C.get_plan((1, 4, 8, 8), (4, 4, 3, 3))
+    monkeypatch.setattr(C, "_lib", two_devices)
+    del two_devices.calls[:]
+    plan.forward(t(1, 4, 8, 8, dtype=torch.float32), t(4, 4, 3, 3, dtype=torch.float32), y=t(*plan.out_shape, dtype=torch.float32),
+                 workspace=t(1 << 16, dtype=torch.uint8))
+    plan.backward_data(t(*plan.out_shape, dtype=torch.float32), t(4, 4, 3, 3, dtype=torch.float32), dx=t(1, 4, 8, 8, dtype=torch.float32),
+                       workspace=t(1 << 16, dtype=torch.uint8))
+    assert two_devices.calls == [("convt_forward", 1), ("convt_backward_data", 1)] and two_devices.now == 0
