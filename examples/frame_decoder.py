@@ -90,7 +90,7 @@ class FrameDecoder:
             with torch.cuda.graph(self.graph):
                 self.step()
         for _ in range(frames):
-            if eager:
+            if eager or self.graph is None:
                 self.step()
             else:
                 self.graph.replay()

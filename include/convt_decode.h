@@ -11,8 +11,9 @@
  * Conventions are those of convt.h: every entry point returns a
  * convt_status; argument errors are found on the host before anything is
  * enqueued; device work is asynchronous on `stream`, a stream of the current
- * device, where all buffers lie; the caller owns every buffer and the workspace; nothing is kept after a call returns and no entry
- * point allocates memory, so every call may be captured into a graph.
+ * device, where all buffers lie; the caller owns every buffer and the
+ * workspace; nothing is kept after a call returns and no entry point
+ * allocates memory, so every call may be captured into a graph.
  * CONVT_ERR_INVALID_ARGUMENT reports a value, shape, stride, alignment or
  * missing pointer that breaks a rule below, CONVT_ERR_UNSUPPORTED a
  * well-formed request that is not computed. Element types are CONVT_DTYPE_F32,
