@@ -54,10 +54,22 @@ class FrameDecoder:
         self.streams = torch.arange(streams, device="cuda")
         self.frame = torch.randn(streams, CHANNELS, generator=g, device="cuda").bfloat16()
         self.out = torch.empty(streams, CHANNELS, frames, device="cuda")  # the upsampler's x
+        self.done = 0  # frames enqueued, known without asking the device
         self.graph = None
+
+    def room_for(self, frames: int) -> None:
+        """ValueError unless `frames` more have room: past it, indexes would leave the output and the page table."""
+        if frames > self.out.shape[2] - self.done:
+            raise ValueError(f"{frames} frames after {self.done}: there is room for {self.out.shape[2]}")
 
     def step(self) -> None:
         """Each stream's next frame, from its last one."""
+        self.room_for(1)
+        self.enqueue()
+        self.done += 1
+
+    def enqueue(self) -> None:
+        """A step's calls, for the stream or the graph that takes them."""
         self.out.scatter_(2, self.lengths.long().view(-1, 1, 1).expand(-1, CHANNELS, 1), self.frame.float().unsqueeze(2))
         slots = C.cache_slots(self.table, self.streams, self.lengths.long(), self.page)
         self.lengths += 1
@@ -77,7 +89,9 @@ class FrameDecoder:
         self.frame.copy_(C.q4_matvec(y, *self.head, x_scale=ys))
 
     def generate(self, frames: int, eager: bool = False) -> torch.Tensor:
-        """The next `frames` frames; returns all so far, [streams, 128, room for frames]."""
+        """The next `frames` frames; returns all so far, [streams, 128, room for frames].
+        ValueError where there is no room for them; nothing is enqueued then."""
+        self.room_for(frames)
         if not eager and self.graph is None and frames > 1:
             # one step outside the graph (it is a frame like any other), then the capture, which runs nothing
             side = torch.cuda.Stream()
@@ -88,12 +102,13 @@ class FrameDecoder:
             frames -= 1
             self.graph = torch.cuda.CUDAGraph()
             with torch.cuda.graph(self.graph):
-                self.step()
+                self.enqueue()
         for _ in range(frames):
             if eager or self.graph is None:
                 self.step()
             else:
                 self.graph.replay()
+                self.done += 1
         return self.out
 
 

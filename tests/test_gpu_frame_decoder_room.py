@@ -15,3 +15,20 @@ def test_single_frames_before_the_graph():
         done = int(a.lengths[0])
         assert torch.equal(a.lengths, b.lengths) and torch.equal(x[:, :, :done], y[:, :, :done])
     assert done == 8 and b.graph is not None
+
+
+def test_no_room_after_replays():
+    """Frames replayed from the graph count too: the one past the room is refused, and nothing is enqueued for it."""
+    from examples.frame_decoder import FrameDecoder
+    m = FrameDecoder(2, 6, width=256, layers=1, heads=8, kv_heads=2)
+    m.generate(4)
+    with pytest.raises(ValueError, match="room"):
+        m.generate(3)
+    x = m.generate(2)
+    torch.cuda.synchronize()
+    assert m.lengths.tolist() == [6, 6] and m.done == 6 and x.isfinite().all()
+    for eager in (False, True):
+        with pytest.raises(ValueError, match="room"):
+            m.generate(1, eager)
+    torch.cuda.synchronize()
+    assert m.lengths.tolist() == [6, 6]
