@@ -363,9 +363,16 @@ def cache_read(cache: KVCache, slots, dtype=None, k=None, v=None, stream=None):
 
 
 def cache_slots(page_table, streams, positions, page_size: int):
-    """The slots (int64) of the tokens at `positions` of `streams` (rows of page_table)."""
-    pages = page_table[streams, torch.div(positions, page_size, rounding_mode="floor")].to(torch.int64)
-    return pages * page_size + positions % page_size
+    """The slots (int64) of the tokens at `positions` of `streams` (rows of page_table). A
+    position before the first or past what the table can hold has slot -1, which is no place of
+    a cache: it is not written, and read as zeros."""
+    width = page_table.shape[1]
+    if width == 0:
+        return torch.full_like(streams + positions, -1, dtype=torch.int64)
+    at = torch.div(positions, page_size, rounding_mode="floor")
+    inside = at.clamp(0, width - 1)
+    slots = page_table[streams, inside].to(torch.int64) * page_size + positions % page_size
+    return slots.masked_fill_(at != inside, -1)
 
 
 def attend_plan(cache: KVCache, q, page_table, scale=None, max_length: Optional[int] = None, out=None,

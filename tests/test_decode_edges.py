@@ -164,3 +164,14 @@ def test_calls_go_to_their_tensors_device(two_devices, monkeypatch):
     plan.backward_data(t(*plan.out_shape, dtype=torch.float32), t(4, 4, 3, 3, dtype=torch.float32), dx=t(1, 4, 8, 8, dtype=torch.float32),
                        workspace=t(1 << 16, dtype=torch.uint8))
     assert two_devices.calls == [("convt_forward", 1), ("convt_backward_data", 1)] and two_devices.now == 0
+
+
+def test_slots_of_positions_outside_the_table():
+    """A position before the first token or past the table has no slot; it took another page's place, or none on the device."""
+    table = torch.tensor([[3, 0], [7, -1]], dtype=torch.int32)
+    got = C.cache_slots(table, torch.tensor([0, 0, 0, 0, 1, 0]), torch.tensor([-1, -16, -17, 32, 31, 31]), 16)
+    assert got.dtype == torch.int64 and got[:4].tolist() == [-1] * 4 and got[4] < 0 and got[5] == 15
+    assert C.cache_slots(table, torch.tensor([1]), torch.tensor([10 ** 9]), 16).tolist() == [-1]
+    assert C.cache_slots(table, torch.tensor(1), torch.arange(-2, 3), 16).tolist() == [-1, -1, 112, 113, 114]
+    assert C.cache_slots(table[:, :0], torch.tensor([0, 1]), torch.tensor([0, 5]), 16).tolist() == [-1, -1]
+    assert C.cache_slots(table, torch.tensor([0, 1], dtype=torch.int64), torch.tensor([17, 1], dtype=torch.int32), 16).tolist() == [1, 113]

@@ -127,3 +127,17 @@ def test_attend_over_one_table_for_all_streams(route):
     lens = torch.tensor([n, 0, 33], dtype=torch.int32, device=DEV)
     got = C.decode_attention(q, cache, table.expand(3, table.shape[1]), lens, route=route)
     assert torch.equal(got, C.decode_attention(q, cache, table.repeat(3, 1), lens, route=route))
+
+
+def test_tokens_without_a_place_are_not_written():
+    cache = C.KVCache.new(4, 2, 16, 64)
+    table = torch.tensor([[2, 1], [0, 3]], dtype=torch.int32, device=DEV)
+    streams, positions = torch.tensor([0, 1, 0, 1], device=DEV), torch.tensor([-1, 32, 5, 10 ** 6], device=DEV)
+    slots = C.cache_slots(table, streams, positions, 16)
+    assert slots.tolist() == [-1, -1, 37, -1]
+    k = rand(4, 2, 64).bfloat16().to(DEV)
+    C.cache_write(cache, k, k, slots)
+    assert torch.equal(cache.k[2, :, 5], k[2]) and torch.equal(cache.v[2, :, 5], k[2])
+    cache.k[2, :, 5], cache.v[2, :, 5] = 0, 0
+    assert (cache.k == 0).all() and (cache.v == 0).all()
+    assert (C.cache_read(cache, slots)[0] == 0).all()
