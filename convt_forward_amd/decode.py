@@ -318,8 +318,8 @@ def _cache_rows(cache: KVCache, k, v, slots) -> CacheRows:
 def cache_write(cache: KVCache, k, v, slots, stream=None) -> KVCache:
     """Write tokens' keys and values (k and v [tokens, kv_heads, head_dim]) into the
     cache at slots (int64 [tokens]), quantised per token and head if the cache
-    is. Tokens whose slot lies outside the cache are not written. Returns
-    the cache."""
+    is. Tokens whose slot lies outside the cache are not written; a slot given twice may be
+    left with parts of both tokens. Returns the cache."""
     rows = _cache_rows(cache, k, v, slots)
     d = cache._desc(k.dtype, "k")
     sh, _ = _launch_stream(stream, cache.device)

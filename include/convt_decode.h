@@ -93,9 +93,10 @@ typedef struct convt_cache_desc {
  * Write tokens' keys and values into the cache: k and v are [tokens][kv_heads]
  * [head_dim] of the element type with the given token and head strides (the
  * last is 1), slots[t] the slot of token t. Tokens whose slot is negative or
- * not below n_pages * page_size are not written. Two tokens with one slot
- * leave one of the two there, which is not said. tokens >= 0; tokens *
- * kv_heads < 2^31.
+ * not below n_pages * page_size are not written. The slots of a call that are
+ * written differ: a place named twice may be left with parts of both tokens
+ * (one's codes, the other's scale); other places are as they should be.
+ * tokens >= 0; tokens * kv_heads < 2^31.
  */
 typedef struct convt_cache_rows {
     int64_t tokens;
