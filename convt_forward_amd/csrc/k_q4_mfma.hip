@@ -54,7 +54,7 @@ struct Q4Args {
     int32_t x_at, x_row;         // LDS with XL: byte offset of x, bytes of a row of it
 };
 
-constexpr int kMaxWaves = 8;  // of a block; 4 with 64 rows of x, for their registers
+constexpr int kMaxWaves = 8;  // of a block
 
 // 8 weights, as they are, in the order (0, 2), (4, 6), (1, 3), (5, 7).
 template <typename E> __device__ __forceinline__ typename Vec8<E>::type unpack(uint32_t w) {
@@ -86,7 +86,7 @@ __device__ __forceinline__ u32x4 transpose_groups(u32x4 w) {
 // NT: tiles of 16 columns a wave, MT: tiles of 16 rows of x, U: chunks of 128 k a
 // stage, XL: x is held in LDS.
 template <typename E, bool X8, int GS, int NT, int MT, int U, bool XL>
-__global__ __launch_bounds__(64 * (MT == 4 ? 4 : kMaxWaves)) void q4_mfma(Q4Args a) {
+__global__ __launch_bounds__(64 * kMaxWaves) void q4_mfma(Q4Args a) {
     typedef typename Vec8<E>::type E8;
     constexpr int XS = X8 ? 1 : 2;
     // x of a chunk in 16-byte pieces of a lane: 8 k each for the products of 32 k, or, of
@@ -335,7 +335,7 @@ constexpr size_t kXLds = 40960;
 
 template <typename E, bool X8, int GS, int NT, int MT> void go(Q4Args a, int wk, int wn, hipStream_t s) {
     // 128 bytes of each column a stage (a whole line) where the registers allow
-    constexpr int U = NT * MT > 4 || MT == 4 || (MT > 1 && NT > 1) ? 1 : 2;
+    constexpr int U = NT * MT > 4 || (MT > 1 && NT > 1) ? 1 : 2;
     const int tiles = (a.n + 15) / 16;
     const int stages = (a.k + 128 * U - 1) / (128 * U);
     a.each = stages > wk ? (stages + wk - 1) / wk : 1;
@@ -363,32 +363,43 @@ template <typename E, bool X8, int GS, int NT, int MT> void go(Q4Args a, int wk,
     q4_mfma<E, X8, GS, NT, MT, U, false><<<grid, 64 * wk * wn, scales > sums ? scales : sums, s>>>(a);
 }
 
-// Waves and tiles. Few columns: one tile a block and 8 waves over k, for as
-// many blocks as there are CUs. Many columns: each block reads all of x, which
-// costs as much as the weights when x is 16 rows (16 x 8192 e4m3 rows x
-// 32768 columns: 34 us with 4 tiles a wave, some 4 more with 2, 9 with 1), so waves
-// take more tiles, from the number of columns on that still leaves blocks for most
-// CUs (16 x 8192 bf16 rows x 12000 columns: 20 us with 4 tiles, 26 with 2; x 8192
-// columns: 19 with 4, 15 with 2). x that fits in LDS is cheap to share (1 x 8192 bf16 x
-// 32768: 3 us less from LDS, with 2 tiles and 2 x 4 waves, than from the caches).
+// Waves and tiles. A block reads all of its rows of x, which costs as much as the
+// weights when x is 16 rows, and blocks beyond one a CU wait for a second turn. So
+// a wave takes the fewest tiles of columns (1, 2 or 4) that leave at most 256
+// blocks, and 4 where no number does; 8 waves share k, but 4 with 4 tiles of 32
+// rows (their registers) or more than 256 blocks (two of them then run on a CU).
+// Rows go in tiles of 16, or of 32 from 17 on; the weights are read again for every
+// 32. Measured, us, on both sides (1, 2, 4 tiles a wave; bf16, k = 4096, groups of 128):
+//   16 rows, 256 and 384 tiles of columns: 7.5, 8.3, 10.4 and 12.1, 8.5, 10.5;
+//            512 and 768: 12.3, 8.7, 10.7 and 17.9, 14.2, 10.9;
+//            4 tiles with 8 and 4 waves at 1024 and 2048: 11.3, 13.4 and 20.7, 19.6;
+//   32 rows, 256 and 384: 11.1, 12.0, 15.4 and 20.0, 12.1, 15.3; 512 and 768: 20.2, 12.4, 15.6
+//            and 28.9, 22.3, 16.0 (2 tiles with 4 waves at 256 and 512: 13.6, 14.4);
+//   128 rows, 128 and 256: 20.0, 12.2, 15.5 and 36.6, 22.3, 15.8.
+// (Tiles of 64 rows were slower at all sizes: 64 rows x 256, 896, 2048 tiles: 19, 39, 77 at
+// their best against 12.6, 26, 50.) x that fits in LDS is cheap to share, and its blocks run
+// several on a CU: one tile and 8 waves, from 1024 tiles on 2 x 4 waves of 2 tiles (1 row: 768
+// tiles 9.3 and 9.6, 1024 11.4 and 10.4, 2048 19.5 and 15.2; 4 rows, 1024: 12.5 and 11.4).
 // The scales of a block's columns fit in 64 KB of LDS: fewer tiles otherwise.
 template <typename E, bool X8, int GS> void run(const Q4Args &a, hipStream_t s) {
     const int tiles = (a.n + 15) / 16;
     const int wide = (a.k / GS + 16) * 2 * 16;  // LDS bytes of a tile's scales
-    const bool four = wide * 4 <= 65536, two = wide * 2 <= 65536;
-    if (a.rows > 32) {
-        if (tiles >= 448 && two) go<E, X8, GS, 2, 4>(a, 4, 1, s);
-        else go<E, X8, GS, 1, 4>(a, 4, 1, s);
-    } else if (a.rows > 16) {
-        if (tiles >= 1024 && four) go<E, X8, GS, 4, 2>(a, 4, 1, s);
-        else if (tiles >= 448 && two) go<E, X8, GS, 2, 2>(a, 4, 1, s);
-        else go<E, X8, GS, 1, 2>(a, 8, 1, s);
-    } else if ((size_t)a.rows * ((a.k + 256) * (X8 ? 1 : 2) + 64) <= kXLds && wide * 4 <= 32768) {
+    if (a.rows <= 16 && (size_t)a.rows * ((a.k + 256) * (X8 ? 1 : 2) + 64) <= kXLds && wide * 4 <= 32768) {
         if (tiles >= 1024) go<E, X8, GS, 2, 1>(a, 4, 2, s);
         else go<E, X8, GS, 1, 1>(a, 8, 1, s);
+        return;
+    }
+    const int64_t row_tiles = a.rows > 16 ? (a.rows + 31) / 32 : 1;
+    auto one_turn = [&](int nt) { return (tiles + nt - 1) / nt * row_tiles <= 256; };
+    int nt = one_turn(1) ? 1 : one_turn(2) ? 2 : 4;
+    while (wide * nt > 65536) nt /= 2;
+    if (a.rows > 16) {
+        if (nt == 4) go<E, X8, GS, 4, 2>(a, 4, 1, s);
+        else if (nt == 2) go<E, X8, GS, 2, 2>(a, 8, 1, s);
+        else go<E, X8, GS, 1, 2>(a, 8, 1, s);
     } else {
-        if (tiles >= 700 && four) go<E, X8, GS, 4, 1>(a, tiles >= 2048 ? 4 : 8, 1, s);
-        else if (tiles >= 448 && two) go<E, X8, GS, 2, 1>(a, 8, 1, s);
+        if (nt == 4) go<E, X8, GS, 4, 1>(a, one_turn(4) ? 8 : 4, 1, s);
+        else if (nt == 2) go<E, X8, GS, 2, 1>(a, 8, 1, s);
         else go<E, X8, GS, 1, 1>(a, 8, 1, s);
     }
 }

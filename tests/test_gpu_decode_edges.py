@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import convt_forward_amd as C
-from tests.decode_util import TYPES, U, attend64, attend_bound, within
+from tests.decode_util import TYPES, U, attend64, attend_bound, rounding, within
 
 pytestmark = pytest.mark.gpu
 
@@ -141,3 +141,21 @@ def test_tokens_without_a_place_are_not_written():
     cache.k[2, :, 5], cache.v[2, :, 5] = 0, 0
     assert (cache.k == 0).all() and (cache.v == 0).all()
     assert (C.cache_read(cache, slots)[0] == 0).all()
+
+
+@pytest.mark.parametrize("rows,n", [(r, n) for r, most in ((7, 256), (16, 256), (17, 256), (32, 256), (33, 128), (64, 128), (65, 85), (130, 51))
+                                    for n in (16 * most, 16 * most + 1, 32 * most + 3, 64 * most, 64 * most + 5)])
+def test_q4_where_the_tiles_change(rows, n):
+    """Both sides of the numbers of columns at which a wave takes 1, 2 or 4 tiles, and 8 or 4 waves share k."""
+    k, group, t = 12288 if rows == 7 else 3200, 64, torch.bfloat16
+    g = torch.Generator(device=DEV).manual_seed(rows + n)
+    w = torch.randint(0, 256, (n, k // 2), generator=g, device=DEV, dtype=torch.uint8)
+    s = (0.02 * (0.5 + torch.rand(n, k // group, generator=g, device=DEV))).to(t)
+    x = torch.randn(rows, k, generator=g, device=DEV).to(t)
+    got = C.q4_matvec(x, w, s, route="auto")
+    w64 = torch.stack([w & 15, w >> 4], -1).view(n, k).double() - 8
+    s64 = s.double().repeat_interleave(group, 1)
+    want = x.double() @ (w64 * s64).t()
+    # sums run over w and 8 x: terms of at most 15 |x|
+    bound = rounding(t, want) * (1 + 2.0 ** -6) + (x.double().abs() @ s64.t()) * (15 * (k / 128 + 64) * U)
+    within(got, want.cpu(), bound.cpu(), f"{rows} x {k} x {n}")
