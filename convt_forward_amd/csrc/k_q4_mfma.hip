@@ -10,8 +10,12 @@
 // mantissa of 16.0 takes 8, for 16 + w: 37 against 34 us for the case below.)
 // The 8 that w is too large by is taken off as 8 sum x of the group: one more
 // product, of x with a constant, whose result is where the group's sum
-// starts. All products are exact in float32, and w in place of w - 8 keeps
-// the sums within a factor of 2. e4m3 rows are widened to E, exactly, for
+// starts. All products are exact in float32; the sums' roundings are those of
+// terms up to 15 |x|, twice the 8 |x| of w - 8 itself. Where most w - 8 are small
+// and x is of one sign the two sums are larger than what is left of them: the error
+// stays 2^-24 of their size (weights of 0 alone, 4096 x in 0 .. 1: up to 1e-4
+// where sum 8 |x| is 16600), which matters to a two-byte result only below
+// 2^-12 of sum 8 |x|. e4m3 rows are widened to E, exactly, for
 // the same products: those on 8-bit operands would take the weights' bytes
 // as they are, but they line their terms up with fewer bits than float32
 // has (off by up to 6e-6 of the terms' magnitudes at k = 128, where these stay
@@ -34,7 +38,8 @@
 // Measured: 16 e4m3 rows x 8192 x 32768 (134 MB of weights): 34 us, 4.1 TB/s; its
 // weights' loads alone take 25, x (read by every block through the caches)
 // most of the rest. One bf16 row: 31 us. One row x 4096 x 4096, 8.7 MB: 4.6
-// us, of which 2.5 are an empty launch and 2.5 a bare read of 8 MB.
+// us a call of a graph (5.4 in a kernel trace); an empty launch takes 2.5, a
+// bare read of 8 MB 2.5 with its launch.
 #include "decode.h"
 #include "kdecode.h"
 
@@ -239,9 +244,6 @@ __global__ __launch_bounds__(64 * kMaxWaves) void q4_mfma(Q4Args a) {
         for (int u = 0; u < U; ++u) chunk(st, c, u);
     };
 
-    // The next stage's loads are issued before this stage's products, and never
-    // under a condition inside the loop (the compiler's waits count the
-    // loads in flight on the path with the fewest).
     Stage s0, s1;
     // this wave's stages follow each other
     const int first = wk * a.each;

@@ -46,13 +46,14 @@ extern "C" {
  * Residual addition and root-mean-square norm:
  *     h[r, i] = x[r, i] + residual[r, i]          (x alone without a residual)
  *     y[r, i] = h[r, i] / sqrt(mean_i h[r, i]^2 + eps) * weight[i]
- * in float32 throughout; residual_out receives h rounded to the element type
- * (the norm itself uses h before that rounding). y is rounded to the element
- * type, or, with quantise = 1, quantised per row: y then holds e4m3 codes
+ * in float32 throughout (a row whose sum of squares is not finite there, |h| of
+ * some 1.8e19, gives 0, or NaN where h is infinite); residual_out receives h
+ * rounded to the element type (the norm itself uses h before that rounding). y
+ * is rounded to the element type, or, with quantise = 1, quantised per row: y then holds e4m3 codes
  * (bytes) and scale one float32 per row.
  * rows >= 0, width in 1 .. 2^24; row strides >= width, those of x and residual
- * also 0 (read only when rows > 1). residual and residual_out are required iff has_residual; scale iff
- * quantise. residual_out may be residual or x itself, and y may be x or
+ * also 0 (read only when rows > 1). residual and residual_out are required iff
+ * has_residual; scale iff quantise. residual_out may be residual or x itself, and y may be x or
  * residual when not quantised and the strides agree (each element is read
  * before its place is written); otherwise outputs overlap no input.
  */
@@ -190,7 +191,9 @@ convt_status convt_attend(const convt_attend_problem *problem, const void *q, co
  * contiguous. x is [rows][k] of the element type, or, with x_quantised = 1,
  * e4m3 codes with x_scale float32 [rows] (the norm's quantised output;
  * x_scale is left out otherwise). y is [rows][n] of the element type. Sums in
- * float32, one rounding.
+ * float32, one rounding. On the matrix cores they run over x * w and 8 x, so
+ * their roundings are those of terms of up to 15 |x| (weights of 0 alone give
+ * about 2^-24 of sum 8 |x|, not always 0).
  * rows >= 0, n >= 0, k >= 0; group a multiple of 8 that divides k; row
  * strides of x >= k or 0 and of y >= n (read only when rows > 1); rows and k below
  * 2^31, n at most 2^26 - 4.
