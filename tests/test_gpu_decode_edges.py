@@ -159,3 +159,18 @@ def test_q4_where_the_tiles_change(rows, n):
     # sums run over w and 8 x: terms of at most 15 |x|
     bound = rounding(t, want) * (1 + 2.0 ** -6) + (x.double().abs() @ s64.t()) * (15 * (k / 128 + 64) * U)
     within(got, want.cpu(), bound.cpu(), f"{rows} x {k} x {n}")
+
+
+@pytest.mark.parametrize("bits", [30.4, 33.6, 36.2, 38.7])
+def test_attend_weights_below_the_relative_steps(bits):
+    """Below 2^-29 of the largest a weight over a float16 cache is off by at most 2^-40, and not dropped."""
+    D, t, others = 64, torch.float16, 500
+    q = torch.ones(1, 1, D, dtype=t)
+    k, v = torch.zeros(1, 1, others + 1, D, dtype=t), (50000 + 4000 * rand(1, 1, others + 1, D).clamp(-3, 3)).to(t)
+    k[0, 0, 0], v[0, 0, 0] = bits * math.log(2) / D, 0
+    cache, table, lens = one_stream(k[0], v[0])
+    out = C.decode_attention(q.to(DEV), cache, table, lens, scale=1.0, route="mfma")
+    want, _, mag, top = attend64(q, k.double(), v.double(), [others + 1], 1.0)
+    bound = attend_bound(want, mag, top, D, others + 1, t, 2.0 ** -11) + others * 2.0 ** -40 * v.double().abs().max()
+    assert (bound < want / 2).all()
+    within(out, want, bound, f"weights of 2^-{bits}")
