@@ -49,13 +49,14 @@ extern "C" {
  * in float32 throughout (a row whose sum of squares is not finite there, |h| of
  * some 1.8e19, gives 0, or NaN where h is infinite); residual_out receives h
  * rounded to the element type (the norm itself uses h before that rounding). y
- * is rounded to the element type, or, with quantise = 1, quantised per row: y then holds e4m3 codes
- * (bytes) and scale one float32 per row.
+ * is rounded to the element type, or, with quantise = 1, quantised per row: y
+ * then holds e4m3 codes (bytes) and scale one float32 per row.
  * rows >= 0, width in 1 .. 2^24; row strides >= width, those of x and residual
  * also 0 (read only when rows > 1). residual and residual_out are required iff
- * has_residual; scale iff quantise. residual_out may be residual or x itself, and y may be x or
- * residual when not quantised and the strides agree (each element is read
- * before its place is written); otherwise outputs overlap no input.
+ * has_residual; scale iff quantise. residual_out may be residual or x itself,
+ * and y may be x or residual when not quantised and the strides agree (each
+ * element is read before its place is written); otherwise outputs overlap no
+ * input.
  */
 typedef struct convt_rms_norm_problem {
     int64_t rows, width;
@@ -140,7 +141,8 @@ convt_status convt_cache_read(const convt_cache_desc *cache, const convt_cache_r
  *
  * heads is a multiple of cache.kv_heads, batch * heads below 2^24; q and out have the given batch and
  * head strides (the last is 1), page_table int32 [batch][table_width] with
- * table_stride (0, or at least table_width) between its rows, lengths int32 [batch]. scale is finite.
+ * table_stride (0, or at least table_width) between its rows, lengths int32
+ * [batch]. scale is finite.
  * Routes: ATTEND_MFMA (two-byte types, head_dim a multiple of 16 and at most
  * 256, page_size a multiple of 16, 16-byte aligned cache rows) on the matrix
  * cores; ATTEND_DIRECT for everything else. route = CONVT_ATTEND_AUTO picks;

@@ -172,5 +172,5 @@ def test_attend_weights_below_the_relative_steps(bits):
     out = C.decode_attention(q.to(DEV), cache, table, lens, scale=1.0, route="mfma")
     want, _, mag, top = attend64(q, k.double(), v.double(), [others + 1], 1.0)
     bound = attend_bound(want, mag, top, D, others + 1, t, 2.0 ** -11) + others * 2.0 ** -40 * v.double().abs().max()
-    assert (bound < want / 2).all()
+    assert (bound < want).all()  # 0 in its place would not pass
     within(out, want, bound, f"weights of 2^-{bits}")
