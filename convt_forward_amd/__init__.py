@@ -524,15 +524,19 @@ def conv_transpose_backward_data(dy, w, x_shape, stride=1, padding=0, dilation=1
     return pl.backward_data(dy, w, dx=dx, workspace=workspace, stream=stream)
 
 
-# The decoding-step operators need torch at import; the rest of this module
-# does not, so they are loaded on first use.
+# The decoding-step operators and those of several new tokens need torch at import;
+# the rest of this module does not, so they are loaded on first use.
 _DECODE = ("ATTEND_ROUTES", "KVCache", "Q4_ROUTES", "attend_plan", "cache_read", "cache_slots", "cache_write",
            "decode_attention", "q4_matvec", "q4_quantise", "rms_norm")
+_EXTEND = ("EXTEND_ROUTES", "cache_append", "tree_attention", "tree_mask", "tree_plan", "window_attention", "window_plan")
 
 
 def __getattr__(name):
-    if name in _DECODE:
-        from . import decode
-        value = globals()[name] = getattr(decode, name)
+    if name in _DECODE or name in _EXTEND:
+        if name in _DECODE:
+            from . import decode as module
+        else:
+            from . import extend as module
+        value = globals()[name] = getattr(module, name)
         return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,51 @@
+// Parameters and launchers of the kernels for several new tokens per stream
+// (host side: checked in extend_api.cpp before any launch).
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stdint.h>
+
+#include "convt_extend.h"
+#include "decode.h"
+
+namespace convt {
+
+struct AppendArgs {
+    CacheArgs c;                  // k and v, the cache, slots
+    const void *q;
+    void *q_out;
+    const int64_t *positions;
+    const float *inv_freq;
+    int64_t q_stride[2][2];       // [q, q_out][token, head]
+    int32_t heads, half;          // half = rotary_dim / 2
+    int32_t interleaved, block_tokens;
+    FastDiv div_rows, div_half;   // by heads + 2 kv_heads, by max(half, 1)
+};
+hipError_t launch_append(const AppendArgs &a, int dtype, int quantised, hipStream_t stream);
+
+struct ExtendArgs {
+    const void *q, *k_cache, *v_cache;
+    const float *k_scale, *v_scale;
+    const int32_t *page_table, *lengths;
+    const int32_t *starts;        // window: NULL for one token per stream
+    const uint64_t *tree;         // tree: not NULL
+    void *out;
+    float *lse;
+    float *part_o, *part_ml;      // workspace: [tokens * heads][chunks][head_dim], [..][chunks][2]
+    int64_t q_stride[3], out_stride[3];  // batch (tree), token, head
+    int64_t k_stride[3], v_stride[3];
+    int64_t tree_stride[2];
+    int64_t table_stride, n_pages;
+    int32_t batch, tokens;        // tokens: rows of q; tree: batch * drafts
+    int32_t drafts;               // tree: new tokens of a stream
+    int32_t heads, kv_heads, share;  // share = heads / kv_heads
+    int32_t head_dim, page_size, max_length;
+    int32_t window, sinks;        // window 0: no limit
+    int32_t chunks, chunk_tokens;
+    float scale_log2e;            // scale * log2(e): the softmax runs on powers of two
+    FastDiv div_page, div_heads, div_drafts;
+};
+hipError_t launch_extend_direct(const ExtendArgs &a, int dtype, int quantised, hipStream_t stream);
+hipError_t launch_extend_join(const ExtendArgs &a, int dtype, hipStream_t stream);
+
+}  // namespace convt

@@ -1,0 +1,251 @@
+// C ABI of the operators of several new tokens per stream (declared in
+// include/convt_extend.h): argument checks, the choice of route and split, and
+// the launches.
+#include <hip/hip_runtime_api.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "decode_checks.h"
+#include "extend.h"
+
+using namespace convt;
+
+namespace {
+
+// Whether the matrix-core kernel serves a cache and q strides (pointers apart).
+bool mfma_serves(const convt_cache_desc &c, const int64_t *q_stride, int n) {
+    if (c.dtype == CONVT_DTYPE_F32 || c.head_dim % 16 != 0 || c.head_dim > 256 || c.page_size % 16 != 0) return false;
+    const int64_t piece = c.quantised ? 16 : 8;  // elements in 16 bytes
+    for (int i = 0; i < 3; ++i)
+        if (c.k_stride[i] % piece != 0 || c.v_stride[i] % piece != 0) return false;
+    for (int i = 0; i < n; ++i)
+        if (q_stride[i] % 8 != 0) return false;
+    return false;
+}
+
+// What window and tree problems are checked for alike, and the info of one
+// whose rows see at most `longest` tokens.
+convt_status extend_check(const convt_cache_desc &c, int64_t max_length, int64_t batch, int64_t tokens, int64_t heads,
+                          const int64_t *q_stride, const int64_t *out_stride, int n_strides, int64_t table_width,
+                          int64_t table_stride, int32_t route, float scale, int64_t longest, convt_extend_info *info) {
+    const convt_status st = check_cache(c);
+    if (st != CONVT_OK) return st;
+    if (batch < 0 || tokens < 0 || heads < 1 || heads % c.kv_heads != 0) return CONVT_ERR_INVALID_ARGUMENT;
+    if (tokens > kMaxBlocks || tokens * heads > kMaxBlocks) return CONVT_ERR_UNSUPPORTED;
+    if (table_width < 0 || table_width > kMaxIndex) return CONVT_ERR_INVALID_ARGUMENT;
+    if (batch > 1 && !row_stride_ok(table_stride, table_width, true)) return CONVT_ERR_INVALID_ARGUMENT;
+    if (max_length < 0 || max_length > kMaxIndex - 4096 || max_length > table_width * c.page_size)
+        return CONVT_ERR_INVALID_ARGUMENT;
+    if (!strides_ok(q_stride, n_strides, 0) || !strides_ok(out_stride, n_strides)) return CONVT_ERR_INVALID_ARGUMENT;
+    if (!isfinite(scale)) return CONVT_ERR_INVALID_ARGUMENT;
+    if (route < CONVT_EXTEND_AUTO || route > CONVT_EXTEND_MFMA) return CONVT_ERR_INVALID_ARGUMENT;
+    const bool mfma = mfma_serves(c, q_stride, n_strides);
+    if (route == CONVT_EXTEND_MFMA && !mfma) return CONVT_ERR_UNSUPPORTED;
+    info->route = mfma && route != CONVT_EXTEND_DIRECT ? CONVT_EXTEND_MFMA : CONVT_EXTEND_DIRECT;
+    int64_t chunk = 2048, chunks = ceil_div(longest, chunk);
+    const int64_t rows = tokens * heads;
+    if (rows >= 2048 || chunks < 1) chunks = 1;
+    if (chunks > 32768) chunks = 32768;
+    chunk = ceil_div(ceil_div(longest > 0 ? longest : 1, chunks), 64) * 64;
+    info->chunks = (int32_t)chunks;
+    info->chunk_tokens = (int32_t)chunk;
+    info->workspace_bytes = chunks > 1 ? rows * chunks * (c.head_dim + 2) * (int64_t)sizeof(float) : 0;
+    info->reserved = 0;
+    return CONVT_OK;
+}
+
+convt_status window_check(const convt_window_problem *p, convt_extend_info *info) {
+    if (!p) return CONVT_ERR_INVALID_ARGUMENT;
+    if (!flag(p->ragged) || p->reserved != 0 || p->window < 0 || p->sinks < 0) return CONVT_ERR_INVALID_ARGUMENT;
+    if (!p->ragged && p->tokens != p->batch) return CONVT_ERR_INVALID_ARGUMENT;
+    int64_t longest = p->max_length;
+    if (p->window > 0 && p->window < longest && p->sinks < longest - p->window) longest = p->window + p->sinks;
+    return extend_check(p->cache, p->max_length, p->batch, p->tokens, p->heads, p->q_stride, p->out_stride, 2, p->table_width,
+                        p->table_stride, p->route, p->scale, longest, info);
+}
+
+convt_status tree_check(const convt_tree_problem *p, convt_extend_info *info) {
+    if (!p) return CONVT_ERR_INVALID_ARGUMENT;
+    if (p->reserved != 0 || p->drafts < 1 || p->batch < 0) return CONVT_ERR_INVALID_ARGUMENT;
+    if (p->drafts > 1024) return CONVT_ERR_UNSUPPORTED;
+    if (!strides_ok(p->tree_stride, 2, 0)) return CONVT_ERR_INVALID_ARGUMENT;
+    return extend_check(p->cache, p->max_length, p->batch, (int64_t)p->batch * p->drafts, p->heads, p->q_stride, p->out_stride, 3,
+                        p->table_width, p->table_stride, p->route, p->scale, p->max_length, info);
+}
+
+// The fields that both problems fill alike.
+ExtendArgs common_args(const convt_cache_desc &c, const convt_extend_info &info, int64_t tokens, int64_t heads, int64_t max_length,
+                       float scale, const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                       const float *v_scale, const int32_t *page_table, const int32_t *lengths, void *out, float *lse,
+                       void *workspace) {
+    ExtendArgs a{};
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.page_table = page_table;
+    a.lengths = lengths;
+    a.out = out;
+    a.lse = lse;
+    a.part_o = (float *)workspace;
+    a.part_ml = (float *)workspace + tokens * heads * info.chunks * c.head_dim;
+    for (int i = 0; i < 3; ++i) {
+        a.k_stride[i] = c.k_stride[i];
+        a.v_stride[i] = c.v_stride[i];
+    }
+    a.n_pages = c.n_pages;
+    a.tokens = (int32_t)tokens;
+    a.heads = (int32_t)heads;
+    a.kv_heads = c.kv_heads;
+    a.share = (int32_t)(heads / c.kv_heads);
+    a.head_dim = c.head_dim;
+    a.page_size = c.page_size;
+    // without pages there is nothing to read
+    a.max_length = c.n_pages > 0 ? (int32_t)max_length : 0;
+    a.chunks = info.chunks;
+    a.chunk_tokens = info.chunk_tokens;
+    a.scale_log2e = (float)((double)scale * 1.4426950408889634074);
+    a.div_page = divisor_of((uint32_t)c.page_size);
+    a.div_heads = divisor_of((uint32_t)heads);
+    a.div_drafts = divisor_of(1);
+    return a;
+}
+
+convt_status launch(const ExtendArgs &a, const convt_cache_desc &c, int route, hipStream_t s) {
+    hipError_t e = launch_extend_direct(a, c.dtype, c.quantised, s);
+    if (e == hipSuccess && a.chunks > 1) e = launch_extend_join(a, c.dtype, s);
+    return device_status(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+convt_status convt_cache_append(const convt_append_problem *problem, const void *q, const void *k, const void *v,
+                                const int64_t *slots, const int64_t *positions, const float *inv_freq, void *k_cache,
+                                void *v_cache, float *k_scale, float *v_scale, void *q_out, void *stream) {
+    if (!problem) return CONVT_ERR_INVALID_ARGUMENT;
+    const convt_append_problem &p = *problem;
+    const convt_cache_desc &c = p.cache;
+    const convt_status st = check_cache(c);
+    if (st != CONVT_OK) return st;
+    if (p.heads < 0 || p.reserved != 0 || !flag(p.interleaved)) return CONVT_ERR_INVALID_ARGUMENT;
+    if (p.rotary_dim < 0 || p.rotary_dim > c.head_dim || p.rotary_dim % 2 != 0) return CONVT_ERR_INVALID_ARGUMENT;
+    const int64_t per_token = (int64_t)p.heads + 2 * (int64_t)c.kv_heads;
+    if (p.rows.tokens < 0 || p.rows.tokens > kMaxIndex || per_token > kMaxIndex || p.rows.tokens * per_token > kMaxIndex)
+        return CONVT_ERR_INVALID_ARGUMENT;
+    // a block's rows, at most 4 tokens', are counted in 32 bits
+    if (per_token > kMaxIndex / 8) return CONVT_ERR_UNSUPPORTED;
+    if (!strides_ok(p.rows.k_stride, 2, 0) || !strides_ok(p.rows.v_stride, 2, 0)) return CONVT_ERR_INVALID_ARGUMENT;
+    if (p.heads > 0 && (!strides_ok(p.q_stride, 2, 0) || !strides_ok(p.q_out_stride, 2))) return CONVT_ERR_INVALID_ARGUMENT;
+    if (!cache_pointers_ok(c, k_cache, v_cache, k_scale, v_scale)) return CONVT_ERR_INVALID_ARGUMENT;
+    if (p.heads == 0 && (q || q_out)) return CONVT_ERR_INVALID_ARGUMENT;
+    if (p.rows.tokens == 0) return CONVT_OK;
+    if (!k || !v || !slots || (p.rotary_dim > 0 && (!positions || !inv_freq))) return CONVT_ERR_INVALID_ARGUMENT;
+    if (p.heads > 0 && (!q || !q_out)) return CONVT_ERR_INVALID_ARGUMENT;
+    AppendArgs a{};
+    a.c.k = k;
+    a.c.v = v;
+    a.c.k_cache = k_cache;
+    a.c.v_cache = v_cache;
+    a.c.k_scale = k_scale;
+    a.c.v_scale = v_scale;
+    a.c.slots = slots;
+    for (int i = 0; i < 2; ++i) {
+        a.c.row_stride[0][i] = p.rows.k_stride[i];
+        a.c.row_stride[1][i] = p.rows.v_stride[i];
+        a.q_stride[0][i] = p.q_stride[i];
+        a.q_stride[1][i] = p.q_out_stride[i];
+    }
+    for (int i = 0; i < 3; ++i) {
+        a.c.cache_stride[0][i] = c.k_stride[i];
+        a.c.cache_stride[1][i] = c.v_stride[i];
+    }
+    a.c.n_slots = c.n_pages * c.page_size;
+    a.c.tokens = p.rows.tokens;
+    a.c.kv_heads = c.kv_heads;
+    a.c.page_size = c.page_size;
+    a.c.head_dim = c.head_dim;
+    a.c.div_page = divisor_of((uint32_t)c.page_size);
+    a.q = q;
+    a.q_out = q_out;
+    a.positions = positions;
+    a.inv_freq = inv_freq;
+    a.heads = p.heads;
+    a.half = p.rotary_dim / 2;
+    a.interleaved = p.interleaved;
+    a.div_rows = divisor_of((uint32_t)per_token);
+    a.div_half = divisor_of((uint32_t)(a.half > 0 ? a.half : 1));
+    a.block_tokens = p.rows.tokens >= 4096 ? 4 : 1;
+    return device_status(launch_append(a, c.dtype, c.quantised, (hipStream_t)stream));
+}
+
+convt_status convt_window_query(const convt_window_problem *problem, convt_extend_info *info) {
+    if (!info) return CONVT_ERR_INVALID_ARGUMENT;
+    return window_check(problem, info);
+}
+
+convt_status convt_window_attend(const convt_window_problem *problem, const void *q, const void *k_cache, const void *v_cache,
+                                 const float *k_scale, const float *v_scale, const int32_t *page_table, const int32_t *lengths,
+                                 const int32_t *starts, void *out, float *lse, void *workspace, void *stream) {
+    convt_extend_info info;
+    const convt_status st = window_check(problem, &info);
+    if (st != CONVT_OK) return st;
+    const convt_window_problem &p = *problem;
+    const convt_cache_desc &c = p.cache;
+    if (!cache_pointers_ok(c, k_cache, v_cache, k_scale, v_scale)) return CONVT_ERR_INVALID_ARGUMENT;
+    if (!p.ragged && starts) return CONVT_ERR_INVALID_ARGUMENT;
+    if (p.batch == 0 || p.tokens == 0) return CONVT_OK;
+    if (!q || !out || !lengths || (p.ragged && !starts) || (p.table_width > 0 && !page_table)) return CONVT_ERR_INVALID_ARGUMENT;
+    if (info.workspace_bytes > 0 && (!workspace || !aligned(workspace, 16))) return CONVT_ERR_INVALID_ARGUMENT;
+    ExtendArgs a = common_args(c, info, p.tokens, p.heads, p.max_length, p.scale, q, k_cache, v_cache, k_scale, v_scale, page_table,
+                               lengths, out, lse, workspace);
+    for (int i = 0; i < 2; ++i) {
+        a.q_stride[1 + i] = p.q_stride[i];
+        a.out_stride[1 + i] = p.out_stride[i];
+    }
+    a.table_stride = p.table_stride;
+    a.batch = p.batch;
+    a.starts = starts;
+    // a window or first tokens beyond the longest stream are all of it
+    a.window = p.window < p.max_length ? (int32_t)p.window : 0;
+    a.sinks = p.sinks < p.max_length ? (int32_t)p.sinks : (int32_t)p.max_length;
+    return launch(a, c, info.route, (hipStream_t)stream);
+}
+
+convt_status convt_tree_query(const convt_tree_problem *problem, convt_extend_info *info) {
+    if (!info) return CONVT_ERR_INVALID_ARGUMENT;
+    return tree_check(problem, info);
+}
+
+convt_status convt_tree_attend(const convt_tree_problem *problem, const void *q, const void *k_cache, const void *v_cache,
+                               const float *k_scale, const float *v_scale, const int32_t *page_table, const int32_t *lengths,
+                               const uint64_t *tree, void *out, float *lse, void *workspace, void *stream) {
+    convt_extend_info info;
+    const convt_status st = tree_check(problem, &info);
+    if (st != CONVT_OK) return st;
+    const convt_tree_problem &p = *problem;
+    const convt_cache_desc &c = p.cache;
+    if (!cache_pointers_ok(c, k_cache, v_cache, k_scale, v_scale)) return CONVT_ERR_INVALID_ARGUMENT;
+    if (p.batch == 0) return CONVT_OK;
+    if (!q || !out || !lengths || !tree || (p.table_width > 0 && !page_table)) return CONVT_ERR_INVALID_ARGUMENT;
+    if (!aligned(tree, 8)) return CONVT_ERR_INVALID_ARGUMENT;
+    if (info.workspace_bytes > 0 && (!workspace || !aligned(workspace, 16))) return CONVT_ERR_INVALID_ARGUMENT;
+    ExtendArgs a = common_args(c, info, (int64_t)p.batch * p.drafts, p.heads, p.max_length, p.scale, q, k_cache, v_cache, k_scale,
+                               v_scale, page_table, lengths, out, lse, workspace);
+    for (int i = 0; i < 3; ++i) {
+        a.q_stride[i] = p.q_stride[i];
+        a.out_stride[i] = p.out_stride[i];
+    }
+    a.tree_stride[0] = p.tree_stride[0];
+    a.tree_stride[1] = p.tree_stride[1];
+    a.table_stride = p.table_stride;
+    a.batch = p.batch;
+    a.drafts = p.drafts;
+    a.div_drafts = divisor_of((uint32_t)p.drafts);
+    a.tree = tree;
+    return launch(a, c, info.route, (hipStream_t)stream);
+}
+
+}  // extern "C"

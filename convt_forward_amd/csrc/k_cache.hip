@@ -23,22 +23,6 @@ namespace {
 
 constexpr int kTokens = 4;
 
-// Place of a slot in the cache; page < 0 if it lies outside.
-struct Place {
-    int32_t page, off;
-};
-__device__ __forceinline__ Place place_of(const CacheArgs &a, int64_t slot) {
-    if (slot < 0 || slot >= a.n_slots) return Place{-1, 0};
-    const uint32_t page = fast_div((uint32_t)slot, a.div_page);
-    return Place{(int32_t)page, (int32_t)((uint32_t)slot - page * (uint32_t)a.page_size)};
-}
-__device__ __forceinline__ int64_t cache_offset(const int64_t *stride, uint32_t head, const Place &p) {
-    return p.page * stride[0] + head * stride[1] + p.off * stride[2];
-}
-__device__ __forceinline__ int64_t scale_offset(const CacheArgs &a, uint32_t head, const Place &p) {
-    return ((int64_t)p.page * a.kv_heads + head) * a.page_size + p.off;
-}
-
 // The lane's piece of a row. FULL: lanes past the row read its first piece.
 template <typename T, bool FULL> __device__ __forceinline__ Raw8<T> load_piece(const T *row, int piece, int n) {
     if constexpr (FULL) {
