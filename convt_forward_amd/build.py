@@ -21,7 +21,8 @@ SOURCES = ["plan.cpp", "api.cpp", "k_misc.hip", "k_phase_gemm.hip", "k_gemm_nchw
            "k_bwd_allphase.hip", "k_bwd_grouped.hip", "k_grouped.hip", "noalloc.hip",
            "decode_api.cpp", "k_rms_norm.hip", "k_cache.hip", "k_attend.hip", "k_attend_mfma.hip",
            "k_q4_matvec.hip", "k_q4_mfma.hip",
-           "extend_api.cpp", "k_append.hip", "k_extend.hip"]
+           "extend_api.cpp", "k_append.hip", "k_extend.hip", "k_extend_bf16.hip", "k_extend_bf16_q8.hip",
+           "k_extend_f16.hip", "k_extend_f16_q8.hip"]
 
 # Packed-FP32 instructions are kept out of every kernel (the target feature is
 # switched off for the device pass; the host pass ignores it with a warning).

@@ -20,14 +20,33 @@ bool mfma_serves(const convt_cache_desc &c, const int64_t *q_stride, int n) {
         if (c.k_stride[i] % piece != 0 || c.v_stride[i] % piece != 0) return false;
     for (int i = 0; i < n; ++i)
         if (q_stride[i] % 8 != 0) return false;
-    return false;
+    return true;
+}
+
+// The form of the matrix-core kernel and its tiles for streams of `each` new
+// tokens (ragged ones: on average).
+struct Shape {
+    bool keys;
+    int64_t block_tokens, head_tiles, stream_tiles, tiles;
+};
+Shape shape_of(int64_t batch, int64_t tokens, int64_t each, bool ragged, int64_t share) {
+    Shape s;
+    s.keys = each * share <= 32;
+    const int64_t rows = s.keys ? 32 : 128;
+    s.block_tokens = share >= rows ? 1 : rows / share;
+    s.head_tiles = ceil_div(share, rows);
+    s.stream_tiles = ragged ? 0 : ceil_div(each, s.block_tokens);
+    // ragged: every stream with rows may end in a tile of its own
+    s.tiles = ragged ? tokens / s.block_tokens + (batch < tokens ? batch : tokens) : batch * s.stream_tiles;
+    return s;
 }
 
 // What window and tree problems are checked for alike, and the info of one
-// whose rows see at most `longest` tokens.
-convt_status extend_check(const convt_cache_desc &c, int64_t max_length, int64_t batch, int64_t tokens, int64_t heads,
-                          const int64_t *q_stride, const int64_t *out_stride, int n_strides, int64_t table_width,
-                          int64_t table_stride, int32_t route, float scale, int64_t longest, convt_extend_info *info) {
+// whose rows see at most `longest` tokens. limited: a window limits them.
+convt_status extend_check(const convt_cache_desc &c, int64_t max_length, int64_t batch, int64_t tokens, int64_t each, bool ragged,
+                          int64_t heads, const int64_t *q_stride, const int64_t *out_stride, int n_strides, int64_t table_width,
+                          int64_t table_stride, int32_t route, float scale, int64_t longest, bool limited, convt_extend_info *info,
+                          Shape *shape) {
     const convt_status st = check_cache(c);
     if (st != CONVT_OK) return st;
     if (batch < 0 || tokens < 0 || heads < 1 || heads % c.kv_heads != 0) return CONVT_ERR_INVALID_ARGUMENT;
@@ -39,14 +58,28 @@ convt_status extend_check(const convt_cache_desc &c, int64_t max_length, int64_t
     if (!strides_ok(q_stride, n_strides, 0) || !strides_ok(out_stride, n_strides)) return CONVT_ERR_INVALID_ARGUMENT;
     if (!isfinite(scale)) return CONVT_ERR_INVALID_ARGUMENT;
     if (route < CONVT_EXTEND_AUTO || route > CONVT_EXTEND_MFMA) return CONVT_ERR_INVALID_ARGUMENT;
-    const bool mfma = mfma_serves(c, q_stride, n_strides);
+    *shape = shape_of(batch, tokens, each, ragged, heads / c.kv_heads);
+    const int64_t blocks = shape->tiles * shape->head_tiles * c.kv_heads;
+    const bool mfma = mfma_serves(c, q_stride, n_strides) && blocks <= kMaxBlocks;
     if (route == CONVT_EXTEND_MFMA && !mfma) return CONVT_ERR_UNSUPPORTED;
     info->route = mfma && route != CONVT_EXTEND_DIRECT ? CONVT_EXTEND_MFMA : CONVT_EXTEND_DIRECT;
-    int64_t chunk = 2048, chunks = ceil_div(longest, chunk);
     const int64_t rows = tokens * heads;
-    if (rows >= 2048 || chunks < 1) chunks = 1;
-    if (chunks > 32768) chunks = 32768;
-    chunk = ceil_div(ceil_div(longest > 0 ? longest : 1, chunks), 64) * 64;
+    int64_t chunks, least;
+    if (info->route == CONVT_EXTEND_MFMA) {
+        // a tile's rows together see what their first and last ones do, in whole tiles of 64 after
+        // groups of 16, the first tokens in tiles of their own
+        if (limited) longest += shape->block_tokens + 2 * 64 + 16;
+        const int64_t slots = 256 * (c.head_dim <= 128 ? 2 : 1);
+        chunks = blocks > 0 ? slots / blocks : 1;
+        least = shape->keys ? 512 : 1024;
+    } else {
+        chunks = rows > 0 ? 2048 / rows : 1;
+        least = 2048;
+    }
+    if (chunks > longest / least) chunks = longest / least;
+    if (chunks < 1) chunks = 1;
+    const int64_t chunk = ceil_div(ceil_div(longest > 0 ? longest : 1, chunks), 64) * 64;
+    chunks = longest > 0 ? ceil_div(longest, chunk) : 1;
     info->chunks = (int32_t)chunks;
     info->chunk_tokens = (int32_t)chunk;
     info->workspace_bytes = chunks > 1 ? rows * chunks * (c.head_dim + 2) * (int64_t)sizeof(float) : 0;
@@ -54,23 +87,24 @@ convt_status extend_check(const convt_cache_desc &c, int64_t max_length, int64_t
     return CONVT_OK;
 }
 
-convt_status window_check(const convt_window_problem *p, convt_extend_info *info) {
+convt_status window_check(const convt_window_problem *p, convt_extend_info *info, Shape *shape) {
     if (!p) return CONVT_ERR_INVALID_ARGUMENT;
     if (!flag(p->ragged) || p->reserved != 0 || p->window < 0 || p->sinks < 0) return CONVT_ERR_INVALID_ARGUMENT;
     if (!p->ragged && p->tokens != p->batch) return CONVT_ERR_INVALID_ARGUMENT;
-    int64_t longest = p->max_length;
-    if (p->window > 0 && p->window < longest && p->sinks < longest - p->window) longest = p->window + p->sinks;
-    return extend_check(p->cache, p->max_length, p->batch, p->tokens, p->heads, p->q_stride, p->out_stride, 2, p->table_width,
-                        p->table_stride, p->route, p->scale, longest, info);
+    const bool limited = p->window > 0 && p->window < p->max_length && p->sinks < p->max_length - p->window;
+    const int64_t each = p->ragged && p->batch > 0 ? ceil_div(p->tokens, p->batch) : 1;
+    return extend_check(p->cache, p->max_length, p->batch, p->tokens, each, p->ragged != 0, p->heads, p->q_stride, p->out_stride, 2,
+                        p->table_width, p->table_stride, p->route, p->scale, limited ? p->window + p->sinks : p->max_length, limited,
+                        info, shape);
 }
 
-convt_status tree_check(const convt_tree_problem *p, convt_extend_info *info) {
+convt_status tree_check(const convt_tree_problem *p, convt_extend_info *info, Shape *shape) {
     if (!p) return CONVT_ERR_INVALID_ARGUMENT;
     if (p->reserved != 0 || p->drafts < 1 || p->batch < 0) return CONVT_ERR_INVALID_ARGUMENT;
     if (p->drafts > 1024) return CONVT_ERR_UNSUPPORTED;
     if (!strides_ok(p->tree_stride, 2, 0)) return CONVT_ERR_INVALID_ARGUMENT;
-    return extend_check(p->cache, p->max_length, p->batch, (int64_t)p->batch * p->drafts, p->heads, p->q_stride, p->out_stride, 3,
-                        p->table_width, p->table_stride, p->route, p->scale, p->max_length, info);
+    return extend_check(p->cache, p->max_length, p->batch, (int64_t)p->batch * p->drafts, p->drafts, false, p->heads, p->q_stride,
+                        p->out_stride, 3, p->table_width, p->table_stride, p->route, p->scale, p->max_length, false, info, shape);
 }
 
 // The fields that both problems fill alike.
@@ -112,8 +146,23 @@ ExtendArgs common_args(const convt_cache_desc &c, const convt_extend_info &info,
     return a;
 }
 
-convt_status launch(const ExtendArgs &a, const convt_cache_desc &c, int route, hipStream_t s) {
-    hipError_t e = launch_extend_direct(a, c.dtype, c.quantised, s);
+convt_status launch(const ExtendArgs &a, const convt_cache_desc &c, const convt_extend_info &info, const Shape &shape, hipStream_t s) {
+    const bool mfma = info.route == CONVT_EXTEND_MFMA && aligned(a.q, 16) && aligned(a.k_cache, 16) && aligned(a.v_cache, 16);
+    hipError_t e;
+    if (mfma) {
+        ExtendTiles t;
+        t.block_tokens = (int32_t)shape.block_tokens;
+        t.head_tiles = (int32_t)shape.head_tiles;
+        t.stream_tiles = (int32_t)shape.stream_tiles;
+        t.tiles = (int32_t)shape.tiles;
+        t.div_kv = divisor_of((uint32_t)a.kv_heads);
+        t.div_head_tiles = divisor_of((uint32_t)t.head_tiles);
+        t.div_stream_tiles = divisor_of((uint32_t)(t.stream_tiles > 0 ? t.stream_tiles : 1));
+        if (c.quantised) e = c.dtype == CONVT_DTYPE_BF16 ? launch_extend_bf16_q8(a, t, shape.keys, s) : launch_extend_f16_q8(a, t, shape.keys, s);
+        else e = c.dtype == CONVT_DTYPE_BF16 ? launch_extend_bf16(a, t, shape.keys, s) : launch_extend_f16(a, t, shape.keys, s);
+    } else {
+        e = launch_extend_direct(a, c.dtype, c.quantised, s);
+    }
     if (e == hipSuccess && a.chunks > 1) e = launch_extend_join(a, c.dtype, s);
     return device_status(e);
 }
@@ -183,14 +232,16 @@ convt_status convt_cache_append(const convt_append_problem *problem, const void 
 
 convt_status convt_window_query(const convt_window_problem *problem, convt_extend_info *info) {
     if (!info) return CONVT_ERR_INVALID_ARGUMENT;
-    return window_check(problem, info);
+    Shape shape;
+    return window_check(problem, info, &shape);
 }
 
 convt_status convt_window_attend(const convt_window_problem *problem, const void *q, const void *k_cache, const void *v_cache,
                                  const float *k_scale, const float *v_scale, const int32_t *page_table, const int32_t *lengths,
                                  const int32_t *starts, void *out, float *lse, void *workspace, void *stream) {
     convt_extend_info info;
-    const convt_status st = window_check(problem, &info);
+    Shape shape;
+    const convt_status st = window_check(problem, &info, &shape);
     if (st != CONVT_OK) return st;
     const convt_window_problem &p = *problem;
     const convt_cache_desc &c = p.cache;
@@ -211,19 +262,21 @@ convt_status convt_window_attend(const convt_window_problem *problem, const void
     // a window or first tokens beyond the longest stream are all of it
     a.window = p.window < p.max_length ? (int32_t)p.window : 0;
     a.sinks = p.sinks < p.max_length ? (int32_t)p.sinks : (int32_t)p.max_length;
-    return launch(a, c, info.route, (hipStream_t)stream);
+    return launch(a, c, info, shape, (hipStream_t)stream);
 }
 
 convt_status convt_tree_query(const convt_tree_problem *problem, convt_extend_info *info) {
     if (!info) return CONVT_ERR_INVALID_ARGUMENT;
-    return tree_check(problem, info);
+    Shape shape;
+    return tree_check(problem, info, &shape);
 }
 
 convt_status convt_tree_attend(const convt_tree_problem *problem, const void *q, const void *k_cache, const void *v_cache,
                                const float *k_scale, const float *v_scale, const int32_t *page_table, const int32_t *lengths,
                                const uint64_t *tree, void *out, float *lse, void *workspace, void *stream) {
     convt_extend_info info;
-    const convt_status st = tree_check(problem, &info);
+    Shape shape;
+    const convt_status st = tree_check(problem, &info, &shape);
     if (st != CONVT_OK) return st;
     const convt_tree_problem &p = *problem;
     const convt_cache_desc &c = p.cache;
@@ -245,7 +298,7 @@ convt_status convt_tree_attend(const convt_tree_problem *problem, const void *q,
     a.drafts = p.drafts;
     a.div_drafts = divisor_of((uint32_t)p.drafts);
     a.tree = tree;
-    return launch(a, c, info.route, (hipStream_t)stream);
+    return launch(a, c, info, shape, (hipStream_t)stream);
 }
 
 }  // extern "C"

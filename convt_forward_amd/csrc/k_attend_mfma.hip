@@ -64,17 +64,6 @@ __device__ __forceinline__ float quad_sum(float v) {
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// Two bfloat16 values with infinities (and NaN) replaced by the largest finite
-// value of their sign, as integers: unsigned, that bounds the negative ones;
-// signed, the positive ones.
-__device__ __forceinline__ uint32_t finite_bf16(uint32_t w) {
-    typedef uint16_t u2 __attribute__((ext_vector_type(2)));
-    typedef int16_t i2 __attribute__((ext_vector_type(2)));
-    const u2 n = __builtin_elementwise_min(__builtin_bit_cast(u2, w), u2{0xff7f, 0xff7f});
-    const i2 v = __builtin_elementwise_min(__builtin_bit_cast(i2, n), i2{0x7f7f, 0x7f7f});
-    return __builtin_bit_cast(uint32_t, v);
-}
-
 template <int BYTES> struct Piece;
 template <> struct Piece<4> { typedef uint32_t type; };
 template <> struct Piece<8> { typedef u32x2 type; };

@@ -54,6 +54,17 @@ template <typename E, bool HI> __device__ __forceinline__ uint32_t e4m3_pair(uin
         return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, scale, HI));
 }
 
+// Two bfloat16 values with infinities (and NaN) replaced by the largest finite
+// value of their sign, as integers: unsigned, that bounds the negative ones;
+// signed, the positive ones.
+__device__ __forceinline__ uint32_t finite_bf16(uint32_t w) {
+    typedef uint16_t u2 __attribute__((ext_vector_type(2)));
+    typedef int16_t i2 __attribute__((ext_vector_type(2)));
+    const u2 n = __builtin_elementwise_min(__builtin_bit_cast(u2, w), u2{0xff7f, 0xff7f});
+    const i2 v = __builtin_elementwise_min(__builtin_bit_cast(i2, n), i2{0x7f7f, 0x7f7f});
+    return __builtin_bit_cast(uint32_t, v);
+}
+
 // 8 elements in the registers they are loaded into.
 template <typename T> struct Raw8 { u32x4 w; };
 template <> struct Raw8<float> { f32x4 lo, hi; };

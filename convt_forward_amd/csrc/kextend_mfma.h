@@ -1,0 +1,692 @@
+// Attention of several new tokens per stream over the paged cache on the
+// matrix cores: two-byte element types, caches of that type or of e4m3 codes.
+// One kernel in two forms, for windows and for trees of drafts:
+//
+//   rows  4 waves of 32 rows (a row: a token and a query head that shares the
+//         kv head); tiles of 64 tokens go through LDS once for the 128 rows, two
+//         buffers, one barrier a tile. For prompts, where the matrix cores
+//         bound it, and large trees.
+//   keys  4 waves with the same 32 rows; each takes every fourth tile of 32
+//         tokens through its own part of LDS, without a barrier until the waves
+//         are joined. For few rows, where reading the cache bounds it.
+//
+//   scores  S^T = K Q^T by v_mfma_f32_32x32x16: A is 32 tokens x 16 dims of K, B
+//           is Q, in registers. A lane then has one row (lane % 32) and 16 of a
+//           sub-tile's 32 tokens, tokens 8 g + 4 (lane / 32) + i: a row's largest
+//           score is over the lane's own values and one lane swap.
+//   values  O^T += V^T P^T: B wants 8 tokens of the lane's row, which are 8
+//           of the scores it holds, tokens 16 s + 4 (lane / 32) + i and those 8
+//           further on; A wants the same tokens of one dim, which two transposing
+//           LDS reads (4 tokens x 16 dims per 16 lanes each) give.
+//   LDS     rows of K are spaced an odd number of 16 bytes modulo 256, those of
+//           V 64 or 192: the reads then take all banks in turn.
+//
+// The running base of a row's exponents moves only when a score passes it by
+// 2^8 (the weights are at most 2^8 then): rescaling O for every new maximum
+// would cost as much as the exponentials.
+//
+// Roundings: Q and K enter as stored (e4m3 codes are exact in bf16 and f16;
+// their scales multiply the float32 scores). Weights meet V
+//   as float16 where V is float16 or e4m3 (its codes are exact there), 2^-11 of
+//   their value. They carry a factor 2^7, so that those down to 2^-21 of
+//   the base keep their 11 bits and smaller ones are off by at most 2^-32
+//   of it. With e4m3 the logarithm of the value's scale is added to the score: the weight
+//   is p times the scale, in float16's range whatever the scales are, and
+//   the sum of p takes it off again.
+//   as the sum of two bfloat16 values (2^-16) in the form for few rows over
+//   bfloat16, where the second product costs nothing beside the loads, and as one
+//   (2^-8) in the form for many, where it would cost a third of the speed.
+//
+// Tokens that only some rows of a tile see: their scores become -infinity by
+// a 64-bit mask per row, and an infinite or NaN value among them (looked for
+// in such tiles only) is taken out of the product, which 0 times it would
+// spoil, and given to the rows that see it.
+#pragma once
+
+#include "extend.h"
+#include "kdecode.h"
+#include "kextend.h"
+
+namespace convt {
+
+namespace {
+
+__device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma32(f16x8 a, f16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+// The other half-wave's value of the same row.
+__device__ __forceinline__ float half_max(float v) {
+    auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float half_sum(float v) {
+    auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+// 4 tokens of the lane's dim: 16 lanes give the addresses of 4 tokens x 16
+// dims (4 dims each) and lane i of them gets dim i.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x2 read_transposed(const char *p) {
+    const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)p);
+    return __builtin_bit_cast(u32x2, v);
+}
+
+// The n lowest of 64 bits.
+__device__ __forceinline__ uint64_t low_bits(int n) {
+    return n <= 0 ? 0 : n >= 64 ? ~(uint64_t)0 : ((uint64_t)1 << n) - 1;
+}
+
+// Two-byte values of a word, by kind: INF the bits of infinity.
+template <uint32_t INF> __device__ __forceinline__ bool word_not_finite(uint32_t w) {
+    return (w & INF) == INF || (w & (INF << 16)) == INF << 16;
+}
+template <uint32_t INF> __device__ __forceinline__ uint32_t word_finite(uint32_t w) {
+    const uint32_t lo = (w & INF) == INF ? 0 : w & 0xffffu, hi = (w & (INF << 16)) == INF << 16 ? 0 : w & 0xffff0000u;
+    return lo | hi;
+}
+// 1 (ONE its bits) where the value is of the kind: 0 infinity, 1 -infinity, 2 NaN.
+template <uint32_t INF, uint32_t ONE> __device__ __forceinline__ uint32_t word_kind(uint32_t w, int kind) {
+    uint32_t r = 0;
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t x = w >> (16 * i) & 0xffffu;
+        const bool is = kind == 0 ? x == INF : kind == 1 ? x == (INF | 0x8000u) : (x & 0x7fffu) > INF;
+        r |= is ? ONE << (16 * i) : 0;
+    }
+    return r;
+}
+
+constexpr int next_pow2(int n) { return n <= 1 ? 1 : 2 * next_pow2((n + 1) / 2); }
+
+// DP: head_dim rounded up to 64, 96, 128 or 256.
+template <typename E, bool Q8, int DP, bool KEYS, bool TREE>
+__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs a, ExtendTiles tl) {
+    typedef typename std::conditional<Q8, _Float16, E>::type EV;  // P and V
+    typedef typename Vec8<E>::type E8;
+    typedef typename Vec8<EV>::type EV8;
+    constexpr bool SPLIT = KEYS && __is_same(EV, __bf16);
+    constexpr float RAISE = __is_same(EV, __bf16) ? 0.0f : 7.0f;  // the weights carry 2^RAISE
+    constexpr uint32_t INF = __is_same(EV, __bf16) ? 0x7f80u : 0x7c00u, ONE = __is_same(EV, __bf16) ? 0x3f80u : 0x3c00u;
+    constexpr int KT = KEYS ? 32 : 64;           // tokens of a tile
+    constexpr int NS = KT / 32, NG = KT / 16;
+    constexpr int ROWS = KEYS ? 32 : 128;        // of a block
+    constexpr int NT = KEYS ? 64 : 256;          // threads that fill a tile
+    constexpr int CS = Q8 ? 1 : 2;               // bytes of a cache element
+    constexpr int CHP = next_pow2(DP * CS / 16); // threads along a row of the cache, 16 bytes each
+    constexpr int RS = NT / CHP;                 // rows they take at a time
+    constexpr int NCH = KT / RS;                 // pieces of a thread
+    constexpr int KSTR = DP * 2 + 16, VSTR = DP == 96 ? 192 : DP * 2 + 64;  // bytes between tokens in LDS
+    constexpr int UNIT = KT * (KSTR + VSTR) + (Q8 ? 3 * KT * 4 : 0);
+    constexpr int NC = DP / 16, ND = DP / 32;
+    __shared__ __attribute__((aligned(16))) char lds[(KEYS ? 4 : 2) * UNIT];
+    __shared__ float m_lds[4][32], l_lds[4][32];
+    __shared__ int bad_lds[2][4];
+
+    const int lane = threadIdx.x % 64, r32 = lane % 32, h = lane / 32;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int tid = KEYS ? lane : (int)threadIdx.x;
+
+    // ---- the block's rows
+    const uint32_t y = fast_div(blockIdx.x, tl.div_kv);
+    const int kvh = (int)(blockIdx.x - y * (uint32_t)a.kv_heads);
+    const uint32_t y2 = fast_div(y, tl.div_head_tiles);
+    const int ht = (int)(y - y2 * (uint32_t)tl.head_tiles);
+    // the last tiles of a stream see most and start first
+    int tile = tl.tiles - 1 - (int)y2;
+    int b, tok0, end;  // the stream, the tile's first token, the end of the stream's tokens
+    if (tl.stream_tiles > 0) {
+        b = (int)fast_div((uint32_t)tile, tl.div_stream_tiles);
+        const int in = tile - b * tl.stream_tiles;
+        const int each = TREE ? a.drafts : 1;
+        tok0 = b * each + in * tl.block_tokens;
+        end = (b + 1) * each;
+    } else {
+        // 64 streams at a time: the tiles up to each of them
+        b = -1;
+        tok0 = end = 0;
+        for (int b0 = 0; b0 < a.batch; b0 += 64) {
+            int s0 = 0, s1 = 0;
+            if (b0 + lane < a.batch) {
+                s0 = a.starts[b0 + lane];
+                s1 = a.starts[b0 + lane + 1];
+            }
+            s0 = s0 < 0 ? 0 : s0 > a.tokens ? a.tokens : s0;
+            s1 = s1 < s0 ? s0 : s1 > a.tokens ? a.tokens : s1;
+            const int n = (s1 - s0 + tl.block_tokens - 1) / tl.block_tokens;
+            int sum = n;
+            for (int d = 1; d < 64; d *= 2) {
+                const int v = __shfl_up(sum, d);
+                if (lane >= d) sum += v;
+            }
+            const uint64_t past = __ballot(sum > tile);
+            if (past) {
+                const int l = __ffsll((unsigned long long)past) - 1;
+                b = b0 + l;
+                tok0 = __shfl(s0, l) + (tile - __shfl(sum - n, l)) * tl.block_tokens;
+                end = __shfl(s1, l);
+                break;
+            }
+            tile -= __shfl(sum, 63);
+        }
+        if (b < 0) return;  // the grid has room for the most tiles there can be
+    }
+    b = __builtin_amdgcn_readfirstlane(b);
+    tok0 = __builtin_amdgcn_readfirstlane(tok0);
+    end = __builtin_amdgcn_readfirstlane(end);
+    const int nt = end - tok0 < tl.block_tokens ? end - tok0 : tl.block_tokens;
+    const int hs = a.share - ht * ROWS < ROWS ? a.share - ht * ROWS : ROWS;  // heads of the tile
+    const int nrows = nt * hs;
+    const int row = KEYS ? r32 : wave * 32 + r32;
+    const int real_row = row < nrows ? row : nrows - 1;  // rows past the last compute as it does and are not stored
+    const int rt = real_row / hs;
+    const int token = tok0 + rt;
+    const int head = kvh * a.share + ht * ROWS + real_row - rt * hs;
+    // tokens of the wave's rows
+    const bool idle = !KEYS && wave * 32 >= nrows;
+    const int last = KEYS || wave * 32 + 31 >= nrows ? nrows - 1 : wave * 32 + 31;
+    const int rt0 = __builtin_amdgcn_readfirstlane(KEYS ? 0 : wave * 32 / hs), rt1 = __builtin_amdgcn_readfirstlane(last / hs);
+
+    // ---- what they see
+    const int len = cut_length(a, b);
+    const int pos0 = TREE ? 0 : len - (end - tok0);  // position of the tile's first token
+    int hi, sink_tiles = 0, base0 = 0;               // the last token that any row sees
+    if constexpr (TREE) {
+        hi = (len + a.drafts < a.max_length ? len + a.drafts : a.max_length) - 1;
+    } else {
+        hi = pos0 + nt - 1;
+        const int lo = a.window > 0 && pos0 >= a.window ? pos0 - a.window + 1 : 0;
+        sink_tiles = ((a.sinks < lo ? a.sinks : lo) + KT - 1) / KT;
+        base0 = lo & ~15;
+        if (base0 < sink_tiles * KT) base0 = sink_tiles * KT;
+    }
+    const int n_tiles = sink_tiles + (hi < base0 ? 0 : (hi - base0) / KT + 1);
+    const int chunk = blockIdx.y;
+    const int per_chunk = a.chunk_tokens / KT;
+    const int j0 = chunk * per_chunk;
+    const int j1 = n_tiles - j0 < per_chunk ? n_tiles : j0 + per_chunk;
+    const int64_t out_row = (int64_t)token * a.heads + head;
+    const int64_t part = out_row * a.chunks + chunk;
+    if (j0 >= n_tiles && chunk > 0) {
+        if ((KEYS ? wave == 0 : true) && row < nrows && h == 0) {
+            a.part_ml[part * 2] = -INFINITY;
+            a.part_ml[part * 2 + 1] = 0.0f;
+        }
+        return;
+    }
+    const int D = a.head_dim;
+    auto tile_base = [&](int j) { return j < sink_tiles ? j * KT : base0 + (j - sink_tiles) * KT; };
+    // whether the rows of the tokens t0 .. t1 (of the tile) see all of a tile, or nothing of it
+    auto all_seen = [&](int base, int t0, int t1) {
+        const int to = base + KT - 1;
+        if constexpr (TREE) return to < len && to <= hi;
+        else return to <= pos0 + t0 && (a.window == 0 || base > pos0 + t1 - a.window || to < a.sinks);
+    };
+    auto none_seen = [&](int base, int t0, int t1) {
+        if constexpr (TREE) return false;
+        else return base > pos0 + t1 || (a.window > 0 && base + KT - 1 <= pos0 + t0 - a.window && base >= a.sinks);
+    };
+    const uint64_t *bits = nullptr;
+    if constexpr (TREE) bits = a.tree + b * a.tree_stride[0] + (token - b * a.drafts) * a.tree_stride[1];
+    // the tokens of a tile that the lane's row sees, `ok` the groups of 16 whose page is there
+    auto seen_bits = [&](int base, uint32_t ok) {
+        uint64_t seen;
+        if constexpr (TREE) {
+            seen = low_bits(len - base);
+            const int d0 = base - len;  // the draft at the tile's first token
+            const int words = (a.drafts + 63) / 64;
+            if (d0 < 0) {
+                if (d0 > -64) seen |= bits[0] << -d0;
+            } else {
+                const int w = d0 >> 6, s = d0 & 63;
+                if (w < words) seen |= bits[w] >> s;
+                if (s > 0 && w + 1 < words) seen |= bits[w + 1] << (64 - s);
+            }
+            seen &= low_bits(hi + 1 - base);
+        } else {
+            const int pos = pos0 + rt;
+            seen = low_bits(pos + 1 - base);
+            if (a.window > 0) seen &= ~low_bits(pos - a.window + 1 - base) | low_bits(a.sinks - base);
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+            if (!(ok >> g & 1)) seen &= ~((uint64_t)0xffff << (16 * g));
+        return seen;
+    };
+
+    // ---- Q, the B operand of the score products; a negative scale turns its sign
+    const float c = a.scale_log2e == 0.0f ? 1.0f : fabsf(a.scale_log2e);
+    E8 q[NC];
+    {
+        const uint16_t *qp = (const uint16_t *)a.q + head * a.q_stride[2];
+        if constexpr (TREE) qp += b * a.q_stride[0] + (token - b * a.drafts) * a.q_stride[1];
+        else qp += token * a.q_stride[1];
+        const uint32_t flip = a.scale_log2e < 0.0f ? 0x80008000u : 0, keep = a.scale_log2e == 0.0f ? 0 : ~0u;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            u32x4 w = {0, 0, 0, 0};
+            if (i * 16 < D) w = *(const u32x4 *)(qp + i * 16 + h * 8);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = (w[k] ^ flip) & keep;
+            q[i] = __builtin_bit_cast(E8, w);
+        }
+    }
+
+    // ---- filling tiles
+    const char *kc = (const char *)a.k_cache, *vc = (const char *)a.v_cache;
+    const int32_t *table = a.page_table + b * a.table_stride;
+    const int r0 = tid / CHP, col = tid % CHP, pieces = D * CS / 16;
+    const bool active = col < pieces;
+    const int64_t k_lane = ((r0 % 16) * a.k_stride[2]) * CS + (active ? col : 0) * 16;
+    const int64_t v_lane = ((r0 % 16) * a.v_stride[2]) * CS + (active ? col : 0) * 16;
+    char *my_lds = KEYS ? lds + wave * UNIT : lds;
+    if (D < DP) {
+        // the dims of K past D, which meet zeros of Q, are zeros; no piece is stored there
+        for (int i = threadIdx.x * 4; i < (int)sizeof(lds); i += 256 * 4) *(uint32_t *)(lds + i) = 0;
+        __syncthreads();
+    }
+    u32x4 kr[NCH], vr[NCH];
+    float ks_r = 0.0f, vs_r = 0.0f;
+    int32_t entry[NG];
+    int entry_off[NG];
+    uint32_t ok_next = 0;  // of the tile in the registers
+    // The pages of a tile's groups of 16 tokens. A group past the end takes the
+    // last one there is; its tokens are masked by their index.
+    auto look_up = [&](int j) {
+        const int base = tile_base(j < j1 ? j : j1 - 1);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            int t = base + 16 * g;
+            t = t < (hi & ~15) ? t : hi & ~15;
+            const int pi = (int)fast_div((uint32_t)t, a.div_page);
+            entry[g] = table[pi];
+            entry_off[g] = t - pi * a.page_size;
+        }
+    };
+    auto load_tile = [&]() {
+        int64_t ko[NG], vo[NG], so[NG];
+        ok_next = 0;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const bool ok = entry[g] >= 0 && entry[g] < a.n_pages;
+            const int64_t page = ok ? entry[g] : 0;
+            ok_next |= ok ? 1u << g : 0;
+            ko[g] = page * a.k_stride[0] + kvh * a.k_stride[1] + entry_off[g] * a.k_stride[2];
+            vo[g] = page * a.v_stride[0] + kvh * a.v_stride[1] + entry_off[g] * a.v_stride[2];
+            if constexpr (Q8) so[g] = (page * a.kv_heads + kvh) * a.page_size + entry_off[g];
+        }
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            int64_t kk, vv;
+            if constexpr (RS <= 16) {
+                constexpr int dummy = 0;
+                (void)dummy;
+                kk = ko[i * RS / 16] + (i * RS % 16) * a.k_stride[2];
+                vv = vo[i * RS / 16] + (i * RS % 16) * a.v_stride[2];
+            } else {
+                kk = ko[i * (RS / 16)];
+                vv = vo[i * (RS / 16)];
+#pragma unroll
+                for (int g = 1; g < RS / 16; ++g) {
+                    kk = r0 / 16 == g ? ko[i * (RS / 16) + g] : kk;
+                    vv = r0 / 16 == g ? vo[i * (RS / 16) + g] : vv;
+                }
+            }
+            kr[i] = *(const u32x4 *)(kc + kk * CS + k_lane);
+            vr[i] = *(const u32x4 *)(vc + vv * CS + v_lane);
+        }
+        if constexpr (Q8) {
+            int64_t at = so[0];
+#pragma unroll
+            for (int g = 1; g < NG; ++g) at = tid / 16 % NG == g ? so[g] : at;
+            ks_r = a.k_scale[at + tid % 16];
+            vs_r = a.v_scale[at + tid % 16];
+        }
+    };
+    // Returns whether the values hold an infinity or NaN, looked for if `edge`:
+    // not all rows see all tokens. Values that no row sees become 0 then.
+    auto store_tile = [&](char *to, int base, bool edge) {
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int r = r0 + i * RS;
+            if (edge) {
+                const bool there = base + r <= hi && (ok_next >> (r / 16) & 1);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) vr[i][k] = there ? vr[i][k] : 0;
+            }
+            char *kp = to + r * KSTR + col * (32 / CS), *vp = to + KT * KSTR + r * VSTR + col * (32 / CS);
+            if constexpr (Q8) {
+                u32x4 kw[2], vw[2];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    kw[k / 2][k % 2 * 2] = e4m3_pair<E, false>(kr[i][k]);
+                    kw[k / 2][k % 2 * 2 + 1] = e4m3_pair<E, true>(kr[i][k]);
+                    vw[k / 2][k % 2 * 2] = e4m3_pair<EV, false>(vr[i][k]);
+                    vw[k / 2][k % 2 * 2 + 1] = e4m3_pair<EV, true>(vr[i][k]);
+                }
+                if (edge)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) bad |= word_not_finite<INF>(vw[k / 4][k % 4]);
+                if (active) {
+                    *(u32x4 *)kp = kw[0];
+                    *(u32x4 *)(kp + 16) = kw[1];
+                    *(u32x4 *)vp = vw[0];
+                    *(u32x4 *)(vp + 16) = vw[1];
+                }
+            } else {
+                if (edge)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) bad |= word_not_finite<INF>(vr[i][k]);
+                if (active) {
+                    *(u32x4 *)kp = kr[i];
+                    *(u32x4 *)vp = vr[i];
+                }
+            }
+        }
+        if constexpr (Q8) {
+            if (tid < KT) {
+                // a scale that is not a number leaves the sum through its score alone
+                float *s = (float *)(to + KT * (KSTR + VSTR));
+                const float v = vs_r < 0x1p-126f ? 0x1p-126f : vs_r;
+                s[tid] = ks_r * c;
+                s[KT + tid] = log2f(v);
+                s[2 * KT + tid] = v == v ? 1.0f / v : 0.0f;
+            }
+        }
+        return bad;
+    };
+
+    f32x16 o[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+    float m = -INFINITY, l = 0.0f;  // the base of the weights (their largest is at most 2^(RAISE + 8)), their sum
+
+    // byte offsets of the lane in a tile of K and of V
+    const int k_at = r32 * KSTR + h * 16;
+    const int v_at = KT * KSTR + (4 * h + lane % 16 / 4) * VSTR + (lane / 16 % 2 * 16 + lane % 4 * 4) * 2;
+
+    auto compute = [&](const char *t, int base, uint32_t ok, bool bad) {
+        const bool partial = ok != (1u << NG) - 1 || !all_seen(base, rt0, rt1);
+        f32x16 s[NS];
+#pragma unroll
+        for (int u = 0; u < NS; ++u) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const u32x4 w = *(const u32x4 *)(t + k_at + u * 32 * KSTR + i * 32);
+                s[u] = mfma32(__builtin_bit_cast(E8, w), q[i], s[u]);
+            }
+        }
+        const float *sc = (const float *)(t + KT * (KSTR + VSTR)) + 4 * h;
+        if constexpr (Q8) {
+#pragma unroll
+            for (int u = 0; u < NS; ++u)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const f32x4 k = *(const f32x4 *)(sc + u * 32 + g * 8), v = *(const f32x4 *)(sc + KT + u * 32 + g * 8);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[u][g * 4 + i] = __builtin_fmaf(s[u][g * 4 + i], k[i], v[i]);
+                }
+        }
+        uint64_t seen = ~(uint64_t)0;
+        if (partial) {
+            seen = seen_bits(base, ok) >> (4 * h);
+#pragma unroll
+            for (int u = 0; u < NS; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    s[u][i] = seen >> (32 * u + 8 * (i / 4) + i % 4) & 1 ? s[u][i] : -INFINITY;
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int u = 0; u < NS; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
+        top = half_max(top);
+        if constexpr (!Q8) top *= c;
+        if (__any(top > m + (RAISE + 8.0f))) {
+            const float up = fmaxf(m, top - RAISE);
+            const float alpha = up == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - up);
+            l *= alpha;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) o[d] *= alpha;
+            m = up;
+        }
+        // scores of -infinity alone so far: any finite base
+        const float from = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int u = 0; u < NS; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                s[u][i] = __builtin_amdgcn_exp2f(Q8 ? s[u][i] - from : __builtin_fmaf(s[u][i], c, -from));
+        if constexpr (Q8) {
+#pragma unroll
+            for (int u = 0; u < NS; ++u)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const f32x4 v = *(const f32x4 *)(sc + 2 * KT + u * 32 + g * 8);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) l = __builtin_fmaf(s[u][g * 4 + i], v[i], l);
+                }
+        } else {
+#pragma unroll
+            for (int u = 0; u < NS; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) l += s[u][i];
+        }
+        u32x4 ph[NS * 2], pl[NS * 2];
+#pragma unroll
+        for (int k = 0; k < NS * 2; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x = s[k / 2][k % 2 * 8 + 2 * i], y = s[k / 2][k % 2 * 8 + 2 * i + 1];
+                ph[k][i] = pack_half2<EV>(x, y);
+                if constexpr (SPLIT)
+                    pl[k][i] = pack_half2<EV>(x - __uint_as_float(ph[k][i] << 16), y - __uint_as_float(ph[k][i] & 0xffff0000u));
+            }
+        auto v_word = [&](int k, int d) {  // tokens of step k, dims of tile d
+            const char *p = t + v_at + 16 * k * VSTR + d * 64;
+            const u32x2 x = read_transposed(p), y = read_transposed(p + 8 * VSTR);
+            return u32x4{x[0], x[1], y[0], y[1]};
+        };
+        if (!(partial && bad)) {
+#pragma unroll
+            for (int k = 0; k < NS * 2; ++k)
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    u32x4 w = v_word(k, d);
+                    o[d] = mfma32(__builtin_bit_cast(EV8, w), __builtin_bit_cast(EV8, ph[k]), o[d]);
+                    if constexpr (SPLIT) {
+                        // the low part may be 0 or negative: an infinite value takes part in the first product only
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w[i] = finite_bf16(w[i]);
+                        o[d] = mfma32(__builtin_bit_cast(EV8, w), __builtin_bit_cast(EV8, pl[k]), o[d]);
+                    }
+                }
+        } else {
+            // finite values, then for each other kind whether the row sees any in the dim
+#pragma unroll
+            for (int k = 0; k < NS * 2; ++k)
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    u32x4 w = v_word(k, d);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i] = word_finite<INF>(w[i]);
+                    o[d] = mfma32(__builtin_bit_cast(EV8, w), __builtin_bit_cast(EV8, ph[k]), o[d]);
+                    if constexpr (SPLIT) o[d] = mfma32(__builtin_bit_cast(EV8, w), __builtin_bit_cast(EV8, pl[k]), o[d]);
+                }
+#pragma unroll 1
+            for (int kind = 0; kind < 3; ++kind) {
+                const float add = kind == 0 ? INFINITY : kind == 1 ? -INFINITY : __builtin_nanf("");
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    f32x16 any;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) any[i] = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < NS * 2; ++k) {
+                        u32x4 w = v_word(k, d), sees;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            w[i] = word_kind<INF, ONE>(w[i], kind);
+                            const int at = 16 * k + 8 * (i / 2) + 2 * (i % 2);
+                            sees[i] = (seen >> at & 1 ? ONE : 0) | (seen >> (at + 1) & 1 ? ONE << 16 : 0);
+                        }
+                        any = mfma32(__builtin_bit_cast(EV8, w), __builtin_bit_cast(EV8, sees), any);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[d][i] = any[i] > 0.0f ? o[d][i] + add : o[d][i];
+                }
+            }
+        }
+    };
+
+    if constexpr (KEYS) {
+        int j = j0 + wave;
+        if (j < j1) {
+            look_up(j);
+            load_tile();
+            look_up(j + 4);
+        }
+        for (; j < j1; j += 4) {
+            const int base = tile_base(j);
+            const bool edge = ok_next != (1u << NG) - 1 || !all_seen(base, 0, nt - 1);
+            const uint32_t ok = ok_next;
+            const bool bad = __any(store_tile(my_lds, base, edge));
+            // the tile is the wave's own: its stores are done before its reads, and those before the next stores
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            load_tile();
+            look_up(j + 8);
+            if (!none_seen(base, 0, nt - 1)) compute(my_lds, base, ok, bad);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
+    } else if (j0 < j1) {
+        auto fill = [&](int j) {
+            const int base = tile_base(j);
+            const bool edge = ok_next != (1u << NG) - 1 || !all_seen(base, 0, nt - 1);
+            const bool bad = __any(store_tile(lds + (j & 1) * UNIT, base, edge));
+            if (lane == 0) bad_lds[j & 1][wave] = bad;
+        };
+        look_up(j0);
+        load_tile();
+        look_up(j0 + 1);
+        fill(j0);
+        uint32_t ok = ok_next;
+        __syncthreads();
+        for (int j = j0; j < j1; ++j) {
+            const int base = tile_base(j);
+            load_tile();  // the next one; past the end the last one again, which is not used
+            look_up(j + 2);
+            const int *bl = bad_lds[j & 1];
+            const bool bad = (bl[0] | bl[1] | bl[2] | bl[3]) != 0;
+            if (!idle && !none_seen(base, rt0, rt1)) compute(lds + (j & 1) * UNIT, base, ok, bad);
+            if (j + 1 < j1) fill(j + 1);
+            ok = ok_next;
+            __syncthreads();
+        }
+    }
+
+    // ---- results: the lane has dims 32 d + 8 g + 4 h + i of its row
+    auto store_row = [&](float mm, float ll, auto value) {
+        // value(d, g): 4 dims of the row
+        const bool whole = a.chunks == 1;
+        const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+        uint16_t *op = nullptr;
+        if (whole) {
+            op = (uint16_t *)a.out + head * a.out_stride[2];
+            if constexpr (TREE) op += b * a.out_stride[0] + (token - b * a.drafts) * a.out_stride[1];
+            else op += token * a.out_stride[1];
+        }
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int at = 32 * d + 8 * g + 4 * h;
+                if (at >= D) continue;
+                const f32x4 v = value(d, g);
+                if (whole) {
+                    typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
+                    f32x4 x;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = ll == 0.0f ? 0.0f : v[i] * inv;
+                    *(u32x2_a2 *)(op + at) = u32x2{pack_half2<E>(x[0], x[1]), pack_half2<E>(x[2], x[3])};
+                } else {
+                    *(f32x4 *)(a.part_o + part * D + at) = v;
+                }
+            }
+        if (h == 0) {
+            if (!whole) {
+                a.part_ml[part * 2] = mm;
+                a.part_ml[part * 2 + 1] = ll;
+            } else if (a.lse) {
+                a.lse[out_row] = (mm + log2f(ll)) * 0.69314718055994531f;
+            }
+        }
+    };
+    l = half_sum(l);
+    if constexpr (!KEYS) {
+        if (row < nrows)
+            store_row(m, l, [&](int d, int g) { return f32x4{o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]}; });
+    } else {
+        // Join the waves: each brings its O to the common base and leaves it in LDS, then takes a quarter of the rows' dims.
+        if (h == 0) {
+            m_lds[wave][r32] = m;
+            l_lds[wave][r32] = l;
+        }
+        __syncthreads();  // every wave is done with its tiles
+        float mm = -INFINITY, ll = 0.0f;
+        for (int w = 0; w < 4; ++w) mm = fmaxf(mm, m_lds[w][r32]);
+        const float from = mm == -INFINITY ? 0.0f : mm;
+        for (int w = 0; w < 4; ++w) ll += l_lds[w][r32] * __builtin_amdgcn_exp2f(m_lds[w][r32] - from);
+        const float f = __builtin_amdgcn_exp2f(m - from);
+        float *ol = (float *)lds;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                f32x4 v;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = o[d][4 * g + i] * f;
+                *(f32x4 *)(ol + ((wave * ND + d) * 4 + g) * 256 + lane * 4) = v;
+            }
+        __syncthreads();
+        if (wave == 0 && row < nrows)
+            store_row(mm, ll, [&](int d, int g) {
+                f32x4 v = *(const f32x4 *)(ol + (d * 4 + g) * 256 + lane * 4);
+                for (int w = 1; w < 4; ++w) v += *(const f32x4 *)(ol + ((w * ND + d) * 4 + g) * 256 + lane * 4);
+                return v;
+            });
+    }
+}
+
+template <typename E, bool Q8, int DP> void run_extend(const ExtendArgs &a, const ExtendTiles &t, bool keys, hipStream_t s) {
+    const dim3 grid((unsigned)t.tiles * (unsigned)t.head_tiles * (unsigned)a.kv_heads, (unsigned)a.chunks);
+    if (a.tree) {
+        if (keys) extend_mfma<E, Q8, DP, true, true><<<grid, 256, 0, s>>>(a, t);
+        else extend_mfma<E, Q8, DP, false, true><<<grid, 256, 0, s>>>(a, t);
+    } else {
+        if (keys) extend_mfma<E, Q8, DP, true, false><<<grid, 256, 0, s>>>(a, t);
+        else extend_mfma<E, Q8, DP, false, false><<<grid, 256, 0, s>>>(a, t);
+    }
+}
+
+template <typename E, bool Q8> hipError_t run_dims(const ExtendArgs &a, const ExtendTiles &t, bool keys, hipStream_t s) {
+    if (a.head_dim <= 64) run_extend<E, Q8, 64>(a, t, keys, s);
+    else if (a.head_dim <= 96) run_extend<E, Q8, 96>(a, t, keys, s);
+    else if (a.head_dim <= 128) run_extend<E, Q8, 128>(a, t, keys, s);
+    else run_extend<E, Q8, 256>(a, t, keys, s);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+}  // namespace convt
