@@ -18,6 +18,9 @@ bool mfma_serves(const convt_cache_desc &c, const int64_t *q_stride, int n) {
     const int64_t piece = c.quantised ? 16 : 8;  // elements in 16 bytes
     for (int i = 0; i < 3; ++i)
         if (c.k_stride[i] % piece != 0 || c.v_stride[i] % piece != 0) return false;
+    // the kernel's factors of a tile's offset, and a lane's bytes within 16 tokens, have 32 bits
+    if (c.k_stride[0] >> 31 || c.v_stride[0] >> 31 || c.k_stride[2] >> 25 || c.v_stride[2] >> 25) return false;
+    if (((int64_t)c.kv_heads * c.page_size) >> 31) return false;
     for (int i = 0; i < n; ++i)
         if (q_stride[i] % 8 != 0) return false;
     return true;

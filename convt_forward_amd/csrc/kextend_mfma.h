@@ -38,9 +38,11 @@
 //   (2^-8) in the form for many, where it would cost a third of the speed.
 //
 // Tokens that only some rows of a tile see: their scores become -infinity by
-// a 64-bit mask per row, and an infinite or NaN value among them (looked for
-// in such tiles only) is taken out of the product, which 0 times it would
-// spoil, and given to the rows that see it.
+// a 64-bit mask per row, and infinite or NaN values among them (looked for
+// in such tiles only) are left out of the product, which 0 times them would
+// spoil. If there were any, a second pass over these tiles gives them to the
+// rows that see them (inside the first one, its registers would have cost the
+// others' prefetch).
 #pragma once
 
 #include "extend.h"
@@ -81,15 +83,12 @@ __device__ __forceinline__ uint64_t low_bits(int n) {
     return n <= 0 ? 0 : n >= 64 ? ~(uint64_t)0 : ((uint64_t)1 << n) - 1;
 }
 
-// Two-byte values of a word, by kind: INF the bits of infinity.
-template <uint32_t INF> __device__ __forceinline__ bool word_not_finite(uint32_t w) {
-    return (w & INF) == INF || (w & (INF << 16)) == INF << 16;
-}
+// A word of two values with infinities and NaN replaced by 0; INF the bits of infinity.
 template <uint32_t INF> __device__ __forceinline__ uint32_t word_finite(uint32_t w) {
     const uint32_t lo = (w & INF) == INF ? 0 : w & 0xffffu, hi = (w & (INF << 16)) == INF << 16 ? 0 : w & 0xffff0000u;
     return lo | hi;
 }
-// 1 (ONE its bits) where the value is of the kind: 0 infinity, 1 -infinity, 2 NaN.
+// 1 (ONE its bits) where a value is of the kind: 0 infinity, 1 -infinity, 2 NaN.
 template <uint32_t INF, uint32_t ONE> __device__ __forceinline__ uint32_t word_kind(uint32_t w, int kind) {
     uint32_t r = 0;
     for (int i = 0; i < 2; ++i) {
@@ -114,21 +113,20 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
     constexpr int KT = KEYS ? 32 : 64;           // tokens of a tile
     constexpr int NS = KT / 32, NG = KT / 16;
     constexpr int ROWS = KEYS ? 32 : 128;        // of a block
-    constexpr int NT = KEYS ? 64 : 256;          // threads that fill a tile
+    constexpr int GW = KEYS ? 2 : 1;             // groups of 16 tokens that a wave fills
     constexpr int CS = Q8 ? 1 : 2;               // bytes of a cache element
-    constexpr int CHP = next_pow2(DP * CS / 16); // threads along a row of the cache, 16 bytes each
-    constexpr int RS = NT / CHP;                 // rows they take at a time
-    constexpr int NCH = KT / RS;                 // pieces of a thread
+    constexpr int CHP = next_pow2(DP * CS / 16); // lanes along a token's row in the cache, 16 bytes each
+    constexpr int RS = 64 / CHP;                 // rows they take at a time
+    constexpr int NCH = 16 / RS;                 // pieces of a lane in a group
     constexpr int KSTR = DP * 2 + 16, VSTR = DP == 96 ? 192 : DP * 2 + 64;  // bytes between tokens in LDS
     constexpr int UNIT = KT * (KSTR + VSTR) + (Q8 ? 3 * KT * 4 : 0);
     constexpr int NC = DP / 16, ND = DP / 32;
     __shared__ __attribute__((aligned(16))) char lds[(KEYS ? 4 : 2) * UNIT];
     __shared__ float m_lds[4][32], l_lds[4][32];
-    __shared__ int bad_lds[2][4];
+    __shared__ int there_lds[2][4];  // whether a tile's groups have pages
 
     const int lane = threadIdx.x % 64, r32 = lane % 32, h = lane / 32;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int tid = KEYS ? lane : (int)threadIdx.x;
 
     // ---- the block's rows
     const uint32_t y = fast_div(blockIdx.x, tl.div_kv);
@@ -275,30 +273,36 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
         }
     }
 
-    // ---- filling tiles
-    const char *kc = (const char *)a.k_cache, *vc = (const char *)a.v_cache;
+    // ---- filling tiles: a wave takes whole groups of 16 tokens, which lie in one page
+    const int r0 = lane / CHP, col = lane % CHP;
+    const bool active = col * (16 / CS) < D;
+    const uint32_t k_tok = (uint32_t)a.k_stride[2] * CS, v_tok = (uint32_t)a.v_stride[2] * CS;  // bytes between tokens
+    const char *kc = (const char *)a.k_cache + kvh * a.k_stride[1] * CS, *vc = (const char *)a.v_cache + kvh * a.v_stride[1] * CS;
+    uint32_t k_lane[NCH], v_lane[NCH];  // the lane's bytes in a group (less than 2^30 by the route's rule)
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+        k_lane[i] = (r0 + i * RS) * k_tok + (active ? col : 0) * 16;
+        v_lane[i] = (r0 + i * RS) * v_tok + (active ? col : 0) * 16;
+    }
     const int32_t *table = a.page_table + b * a.table_stride;
-    const int r0 = tid / CHP, col = tid % CHP, pieces = D * CS / 16;
-    const bool active = col < pieces;
-    const int64_t k_lane = ((r0 % 16) * a.k_stride[2]) * CS + (active ? col : 0) * 16;
-    const int64_t v_lane = ((r0 % 16) * a.v_stride[2]) * CS + (active ? col : 0) * 16;
+    const int g0 = KEYS ? 0 : wave;  // the wave's first group of a tile
     char *my_lds = KEYS ? lds + wave * UNIT : lds;
     if (D < DP) {
         // the dims of K past D, which meet zeros of Q, are zeros; no piece is stored there
         for (int i = threadIdx.x * 4; i < (int)sizeof(lds); i += 256 * 4) *(uint32_t *)(lds + i) = 0;
         __syncthreads();
     }
-    u32x4 kr[NCH], vr[NCH];
+    u32x4 kr[GW][NCH], vr[GW][NCH];
     float ks_r = 0.0f, vs_r = 0.0f;
-    int32_t entry[NG];
-    int entry_off[NG];
-    uint32_t ok_next = 0;  // of the tile in the registers
-    // The pages of a tile's groups of 16 tokens. A group past the end takes the
-    // last one there is; its tokens are masked by their index.
+    int32_t entry[GW];
+    int entry_off[GW];
+    uint32_t there = 0;  // the groups of the tile in the registers whose page is there
+    // The pages of a tile's groups. A group past the end takes the last one
+    // there is; its tokens are masked by their index.
     auto look_up = [&](int j) {
-        const int base = tile_base(j < j1 ? j : j1 - 1);
+        const int base = tile_base(j < j1 ? j : j1 - 1) + 16 * g0;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
+        for (int g = 0; g < GW; ++g) {
             int t = base + 16 * g;
             t = t < (hi & ~15) ? t : hi & ~15;
             const int pi = (int)fast_div((uint32_t)t, a.div_page);
@@ -307,94 +311,90 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
         }
     };
     auto load_tile = [&]() {
-        int64_t ko[NG], vo[NG], so[NG];
-        ok_next = 0;
+        there = 0;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
+        for (int g = 0; g < GW; ++g) {
             const bool ok = entry[g] >= 0 && entry[g] < a.n_pages;
-            const int64_t page = ok ? entry[g] : 0;
-            ok_next |= ok ? 1u << g : 0;
-            ko[g] = page * a.k_stride[0] + kvh * a.k_stride[1] + entry_off[g] * a.k_stride[2];
-            vo[g] = page * a.v_stride[0] + kvh * a.v_stride[1] + entry_off[g] * a.v_stride[2];
-            if constexpr (Q8) so[g] = (page * a.kv_heads + kvh) * a.page_size + entry_off[g];
-        }
+            const uint32_t page = ok ? entry[g] : 0, off = entry_off[g];
+            there |= ok ? 1u << g : 0;
+            // strides of less than 2^31 elements: 32-bit factors
+            const char *kp = kc + ((uint64_t)page * (uint32_t)a.k_stride[0] * CS + (uint64_t)off * k_tok);
+            const char *vp = vc + ((uint64_t)page * (uint32_t)a.v_stride[0] * CS + (uint64_t)off * v_tok);
 #pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-            int64_t kk, vv;
-            if constexpr (RS <= 16) {
-                constexpr int dummy = 0;
-                (void)dummy;
-                kk = ko[i * RS / 16] + (i * RS % 16) * a.k_stride[2];
-                vv = vo[i * RS / 16] + (i * RS % 16) * a.v_stride[2];
-            } else {
-                kk = ko[i * (RS / 16)];
-                vv = vo[i * (RS / 16)];
-#pragma unroll
-                for (int g = 1; g < RS / 16; ++g) {
-                    kk = r0 / 16 == g ? ko[i * (RS / 16) + g] : kk;
-                    vv = r0 / 16 == g ? vo[i * (RS / 16) + g] : vv;
-                }
+            for (int i = 0; i < NCH; ++i) {
+                kr[g][i] = *(const u32x4 *)(kp + k_lane[i]);
+                vr[g][i] = *(const u32x4 *)(vp + v_lane[i]);
             }
-            kr[i] = *(const u32x4 *)(kc + kk * CS + k_lane);
-            vr[i] = *(const u32x4 *)(vc + vv * CS + v_lane);
-        }
-        if constexpr (Q8) {
-            int64_t at = so[0];
-#pragma unroll
-            for (int g = 1; g < NG; ++g) at = tid / 16 % NG == g ? so[g] : at;
-            ks_r = a.k_scale[at + tid % 16];
-            vs_r = a.v_scale[at + tid % 16];
+            if constexpr (Q8) {
+                const uint64_t at = (uint64_t)page * (uint32_t)(a.kv_heads * a.page_size) + (uint32_t)(kvh * a.page_size + (int)off);
+                // lanes 16 g .. of the groups' tokens; the others read what they do not use
+                const float k = a.k_scale[at + (uint32_t)(lane % 16)], v = a.v_scale[at + (uint32_t)(lane % 16)];
+                ks_r = GW == 1 || lane / 16 == g ? k : ks_r;
+                vs_r = GW == 1 || lane / 16 == g ? v : vs_r;
+            }
         }
     };
-    // Returns whether the values hold an infinity or NaN, looked for if `edge`:
-    // not all rows see all tokens. Values that no row sees become 0 then.
-    auto store_tile = [&](char *to, int base, bool edge) {
+    // edge: some row of the block does not see some token. Values that no
+    // row sees become 0 then, infinities and NaN too unless `raw`; returns
+    // whether there were any.
+    auto store_tile = [&](char *to, int base, bool edge, bool raw) {
         bool bad = false;
+        const bool cut = edge || there != (1u << GW) - 1;
 #pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-            const int r = r0 + i * RS;
-            if (edge) {
-                const bool there = base + r <= hi && (ok_next >> (r / 16) & 1);
+        for (int g = 0; g < GW; ++g)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) vr[i][k] = there ? vr[i][k] : 0;
+            for (int i = 0; i < NCH; ++i) {
+                const int r = 16 * (g0 + g) + r0 + i * RS;
+                if (cut) {
+                    const bool seen = base + r <= hi && (there >> g & 1);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) vr[g][i][k] = seen ? vr[g][i][k] : 0;
+                }
+                char *kp = to + r * KSTR + col * (32 / CS), *vp = to + KT * KSTR + r * VSTR + col * (32 / CS);
+                if constexpr (Q8) {
+                    u32x4 kw[2], vw[2];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        kw[k / 2][k % 2 * 2] = e4m3_pair<E, false>(kr[g][i][k]);
+                        kw[k / 2][k % 2 * 2 + 1] = e4m3_pair<E, true>(kr[g][i][k]);
+                        vw[k / 2][k % 2 * 2] = e4m3_pair<EV, false>(vr[g][i][k]);
+                        vw[k / 2][k % 2 * 2 + 1] = e4m3_pair<EV, true>(vr[g][i][k]);
+                    }
+                    if (edge)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t w = word_finite<INF>(vw[k / 4][k % 4]);
+                            bad |= w != vw[k / 4][k % 4];
+                            vw[k / 4][k % 4] = raw ? vw[k / 4][k % 4] : w;
+                        }
+                    if (active) {
+                        *(u32x4 *)kp = kw[0];
+                        *(u32x4 *)(kp + 16) = kw[1];
+                        *(u32x4 *)vp = vw[0];
+                        *(u32x4 *)(vp + 16) = vw[1];
+                    }
+                } else {
+                    if (edge)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t w = word_finite<INF>(vr[g][i][k]);
+                            bad |= w != vr[g][i][k];
+                            vr[g][i][k] = raw ? vr[g][i][k] : w;
+                        }
+                    if (active) {
+                        *(u32x4 *)kp = kr[g][i];
+                        *(u32x4 *)vp = vr[g][i];
+                    }
+                }
             }
-            char *kp = to + r * KSTR + col * (32 / CS), *vp = to + KT * KSTR + r * VSTR + col * (32 / CS);
-            if constexpr (Q8) {
-                u32x4 kw[2], vw[2];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    kw[k / 2][k % 2 * 2] = e4m3_pair<E, false>(kr[i][k]);
-                    kw[k / 2][k % 2 * 2 + 1] = e4m3_pair<E, true>(kr[i][k]);
-                    vw[k / 2][k % 2 * 2] = e4m3_pair<EV, false>(vr[i][k]);
-                    vw[k / 2][k % 2 * 2 + 1] = e4m3_pair<EV, true>(vr[i][k]);
-                }
-                if (edge)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) bad |= word_not_finite<INF>(vw[k / 4][k % 4]);
-                if (active) {
-                    *(u32x4 *)kp = kw[0];
-                    *(u32x4 *)(kp + 16) = kw[1];
-                    *(u32x4 *)vp = vw[0];
-                    *(u32x4 *)(vp + 16) = vw[1];
-                }
-            } else {
-                if (edge)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) bad |= word_not_finite<INF>(vr[i][k]);
-                if (active) {
-                    *(u32x4 *)kp = kr[i];
-                    *(u32x4 *)vp = vr[i];
-                }
-            }
-        }
         if constexpr (Q8) {
-            if (tid < KT) {
+            if (lane < 16 * GW) {
                 // a scale that is not a number leaves the sum through its score alone
-                float *s = (float *)(to + KT * (KSTR + VSTR));
+                float *s = (float *)(to + KT * (KSTR + VSTR)) + 16 * g0 + lane;
                 const float v = vs_r < 0x1p-126f ? 0x1p-126f : vs_r;
-                s[tid] = ks_r * c;
-                s[KT + tid] = log2f(v);
-                s[2 * KT + tid] = v == v ? 1.0f / v : 0.0f;
+                s[0] = ks_r * c;
+                s[KT] = log2f(v);
+                s[2 * KT] = v == v ? 1.0f / v : 0.0f;
             }
         }
         return bad;
@@ -411,7 +411,12 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
     const int k_at = r32 * KSTR + h * 16;
     const int v_at = KT * KSTR + (4 * h + lane % 16 / 4) * VSTR + (lane / 16 % 2 * 16 + lane % 4 * 4) * 2;
 
-    auto compute = [&](const char *t, int base, uint32_t ok, bool bad) {
+    auto v_word = [&](const char *t, int k, int d) {  // 8 tokens of step k of 16, a dim of tile d
+        const char *p = t + v_at + 16 * k * VSTR + d * 64;
+        const u32x2 x = read_transposed(p), y = read_transposed(p + 8 * VSTR);
+        return u32x4{x[0], x[1], y[0], y[1]};
+    };
+    auto compute = [&](const char *t, int base, uint32_t ok) {
         const bool partial = ok != (1u << NG) - 1 || !all_seen(base, rt0, rt1);
         f32x16 s[NS];
 #pragma unroll
@@ -435,9 +440,8 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
                     for (int i = 0; i < 4; ++i) s[u][g * 4 + i] = __builtin_fmaf(s[u][g * 4 + i], k[i], v[i]);
                 }
         }
-        uint64_t seen = ~(uint64_t)0;
         if (partial) {
-            seen = seen_bits(base, ok) >> (4 * h);
+            const uint64_t seen = seen_bits(base, ok) >> (4 * h);
 #pragma unroll
             for (int u = 0; u < NS; ++u)
 #pragma unroll
@@ -491,64 +495,55 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
                 if constexpr (SPLIT)
                     pl[k][i] = pack_half2<EV>(x - __uint_as_float(ph[k][i] << 16), y - __uint_as_float(ph[k][i] & 0xffff0000u));
             }
-        auto v_word = [&](int k, int d) {  // tokens of step k, dims of tile d
-            const char *p = t + v_at + 16 * k * VSTR + d * 64;
-            const u32x2 x = read_transposed(p), y = read_transposed(p + 8 * VSTR);
-            return u32x4{x[0], x[1], y[0], y[1]};
-        };
-        if (!(partial && bad)) {
 #pragma unroll
-            for (int k = 0; k < NS * 2; ++k)
+        for (int k = 0; k < NS * 2; ++k)
 #pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    u32x4 w = v_word(k, d);
-                    o[d] = mfma32(__builtin_bit_cast(EV8, w), __builtin_bit_cast(EV8, ph[k]), o[d]);
-                    if constexpr (SPLIT) {
-                        // the low part may be 0 or negative: an infinite value takes part in the first product only
+            for (int d = 0; d < ND; ++d) {
+                u32x4 w = v_word(t, k, d);
+                o[d] = mfma32(__builtin_bit_cast(EV8, w), __builtin_bit_cast(EV8, ph[k]), o[d]);
+                if constexpr (SPLIT) {
+                    // the low part may be 0 or negative: an infinite value takes part in the first product only
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) w[i] = finite_bf16(w[i]);
-                        o[d] = mfma32(__builtin_bit_cast(EV8, w), __builtin_bit_cast(EV8, pl[k]), o[d]);
-                    }
+                    for (int i = 0; i < 4; ++i) w[i] = finite_bf16(w[i]);
+                    o[d] = mfma32(__builtin_bit_cast(EV8, w), __builtin_bit_cast(EV8, pl[k]), o[d]);
                 }
-        } else {
-            // finite values, then for each other kind whether the row sees any in the dim
-#pragma unroll
-            for (int k = 0; k < NS * 2; ++k)
-#pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    u32x4 w = v_word(k, d);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = word_finite<INF>(w[i]);
-                    o[d] = mfma32(__builtin_bit_cast(EV8, w), __builtin_bit_cast(EV8, ph[k]), o[d]);
-                    if constexpr (SPLIT) o[d] = mfma32(__builtin_bit_cast(EV8, w), __builtin_bit_cast(EV8, pl[k]), o[d]);
-                }
+            }
+    };
+    // Infinities and NaN of a tile that not all rows see: for each kind, whether the row sees one in the dim.
+    auto add_kinds = [&](const char *t, int base) {
+        const uint64_t seen = seen_bits(base, ~0u) >> (4 * h);
 #pragma unroll 1
-            for (int kind = 0; kind < 3; ++kind) {
-                const float add = kind == 0 ? INFINITY : kind == 1 ? -INFINITY : __builtin_nanf("");
+        for (int kind = 0; kind < 3; ++kind) {
+            const float add = kind == 0 ? INFINITY : kind == 1 ? -INFINITY : __builtin_nanf("");
 #pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    f32x16 any;
+            for (int d = 0; d < ND; ++d) {
+                f32x16 any;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) any[i] = 0.0f;
+                for (int i = 0; i < 16; ++i) any[i] = 0.0f;
 #pragma unroll
-                    for (int k = 0; k < NS * 2; ++k) {
-                        u32x4 w = v_word(k, d), sees;
+                for (int k = 0; k < NS * 2; ++k) {
+                    u32x4 w = v_word(t, k, d), sees;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            w[i] = word_kind<INF, ONE>(w[i], kind);
-                            const int at = 16 * k + 8 * (i / 2) + 2 * (i % 2);
-                            sees[i] = (seen >> at & 1 ? ONE : 0) | (seen >> (at + 1) & 1 ? ONE << 16 : 0);
-                        }
-                        any = mfma32(__builtin_bit_cast(EV8, w), __builtin_bit_cast(EV8, sees), any);
+                    for (int i = 0; i < 4; ++i) {
+                        w[i] = word_kind<INF, ONE>(w[i], kind);
+                        const int at = 16 * k + 8 * (i / 2) + 2 * (i % 2);
+                        sees[i] = (seen >> at & 1 ? ONE : 0) | (seen >> (at + 1) & 1 ? ONE << 16 : 0);
                     }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[d][i] = any[i] > 0.0f ? o[d][i] + add : o[d][i];
+                    any = mfma32(__builtin_bit_cast(EV8, w), __builtin_bit_cast(EV8, sees), any);
                 }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[d][i] = any[i] > 0.0f ? o[d][i] + add : o[d][i];
             }
         }
     };
 
+    bool bad = false;  // a tile that not all rows see held infinities or NaN
     if constexpr (KEYS) {
+        // the tile is the wave's own: its stores are done before its reads, and those before the next stores
+        auto own_order = [&]() {
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        };
         int j = j0 + wave;
         if (j < j1) {
             look_up(j);
@@ -557,42 +552,60 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
         }
         for (; j < j1; j += 4) {
             const int base = tile_base(j);
-            const bool edge = ok_next != (1u << NG) - 1 || !all_seen(base, 0, nt - 1);
-            const uint32_t ok = ok_next;
-            const bool bad = __any(store_tile(my_lds, base, edge));
-            // the tile is the wave's own: its stores are done before its reads, and those before the next stores
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            load_tile();
+            const uint32_t ok = there;
+            bad |= store_tile(my_lds, base, !all_seen(base, 0, nt - 1), false);
+            own_order();
+            load_tile();  // the wave's next one; past the end the last one, which is not used
             look_up(j + 8);
-            if (!none_seen(base, 0, nt - 1)) compute(my_lds, base, ok, bad);
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
+            if (!none_seen(base, 0, nt - 1)) compute(my_lds, base, ok);
+            own_order();
         }
+        if (__any(bad))
+            for (j = j0 + wave; j < j1; j += 4) {
+                const int base = tile_base(j);
+                if (all_seen(base, 0, nt - 1)) continue;
+                look_up(j);
+                load_tile();
+                store_tile(my_lds, base, true, true);
+                own_order();
+                add_kinds(my_lds, base);
+                own_order();
+            }
     } else if (j0 < j1) {
-        auto fill = [&](int j) {
+        auto fill = [&](int j, int buffer, bool raw) {
             const int base = tile_base(j);
-            const bool edge = ok_next != (1u << NG) - 1 || !all_seen(base, 0, nt - 1);
-            const bool bad = __any(store_tile(lds + (j & 1) * UNIT, base, edge));
-            if (lane == 0) bad_lds[j & 1][wave] = bad;
+            bad |= store_tile(lds + buffer * UNIT, base, !all_seen(base, 0, nt - 1), raw);
+            if (lane == 0) there_lds[buffer][wave] = there;
         };
         look_up(j0);
         load_tile();
         look_up(j0 + 1);
-        fill(j0);
-        uint32_t ok = ok_next;
+        fill(j0, j0 & 1, false);
         __syncthreads();
         for (int j = j0; j < j1; ++j) {
             const int base = tile_base(j);
-            load_tile();  // the next one; past the end the last one again, which is not used
+            load_tile();  // the next one; past the end the last one, which is not used
             look_up(j + 2);
-            const int *bl = bad_lds[j & 1];
-            const bool bad = (bl[0] | bl[1] | bl[2] | bl[3]) != 0;
-            if (!idle && !none_seen(base, rt0, rt1)) compute(lds + (j & 1) * UNIT, base, ok, bad);
-            if (j + 1 < j1) fill(j + 1);
-            ok = ok_next;
+            if (!idle && !none_seen(base, rt0, rt1)) {
+                uint32_t ok = 0;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) ok |= (uint32_t)__builtin_amdgcn_readfirstlane(there_lds[j & 1][w]) << w;
+                compute(lds + (j & 1) * UNIT, base, ok);
+            }
+            if (j + 1 < j1) fill(j + 1, (j + 1) & 1, false);
             __syncthreads();
         }
+        if (__syncthreads_or(bad))
+            for (int j = j0; j < j1; ++j) {
+                const int base = tile_base(j);
+                if (all_seen(base, 0, nt - 1)) continue;
+                look_up(j);
+                load_tile();
+                fill(j, 0, true);
+                __syncthreads();
+                if (!idle) add_kinds(lds, base);
+                __syncthreads();
+            }
     }
 
     // ---- results: the lane has dims 32 d + 8 g + 4 h + i of its row
