@@ -123,7 +123,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
     constexpr int NC = DP / 16, ND = DP / 32;
     __shared__ __attribute__((aligned(16))) char lds[(KEYS ? 4 : 2) * UNIT];
     __shared__ float m_lds[4][32], l_lds[4][32];
-    __shared__ int there_lds[2][4];  // whether a tile's groups have pages
+    __shared__ int there_lds[2];  // whether a tile's groups have pages, a byte each
 
     const int lane = threadIdx.x % 64, r32 = lane % 32, h = lane / 32;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -191,13 +191,14 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
     // ---- what they see
     const int len = cut_length(a, b);
     const int pos0 = TREE ? 0 : len - (end - tok0);  // position of the tile's first token
-    int hi, sink_tiles = 0, base0 = 0;               // the last token that any row sees
+    int hi, first_seen = 0, sink_tiles = 0, base0 = 0;  // the last token that any row sees; the first ones before the window
     if constexpr (TREE) {
         hi = (len + a.drafts < a.max_length ? len + a.drafts : a.max_length) - 1;
     } else {
         hi = pos0 + nt - 1;
         const int lo = a.window > 0 && pos0 >= a.window ? pos0 - a.window + 1 : 0;
-        sink_tiles = ((a.sinks < lo ? a.sinks : lo) + KT - 1) / KT;
+        first_seen = a.sinks < lo ? a.sinks : lo;
+        sink_tiles = (first_seen + KT - 1) / KT;
         base0 = lo & ~15;
         if (base0 < sink_tiles * KT) base0 = sink_tiles * KT;
     }
@@ -217,16 +218,25 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
     }
     const int D = a.head_dim;
     auto tile_base = [&](int j) { return j < sink_tiles ? j * KT : base0 + (j - sink_tiles) * KT; };
-    // whether the rows of the tokens t0 .. t1 (of the tile) see all of a tile, or nothing of it
-    auto all_seen = [&](int base, int t0, int t1) {
-        const int to = base + KT - 1;
-        if constexpr (TREE) return to < len && to <= hi;
-        else return to <= pos0 + t0 && (a.window == 0 || base > pos0 + t1 - a.window || to < a.sinks);
+    // The tiles that the rows of the tokens t0 .. t1 (of the block) all see whole: those before `first`,
+    // of the first tokens, and from..to - 1.
+    struct Whole {
+        int first, from, to;
+        __device__ bool has(int j) const { return j < first || (j >= from && j < to); }
     };
-    auto none_seen = [&](int base, int t0, int t1) {
-        if constexpr (TREE) return false;
-        else return base > pos0 + t1 || (a.window > 0 && base + KT - 1 <= pos0 + t0 - a.window && base >= a.sinks);
+    auto whole_tiles = [&](int t0, int t1) {
+        Whole w{0, 0, 0};
+        if constexpr (TREE) {
+            w.to = (len < hi + 1 ? len : hi + 1) / KT;
+        } else {
+            const int to = pos0 + t0 + 1 - base0, from = a.window > 0 ? pos0 + t1 - a.window + 1 - base0 : 0;
+            w.first = first_seen / KT;
+            w.from = sink_tiles + (from > 0 ? (from + KT - 1) / KT : 0);
+            w.to = sink_tiles + (to > 0 ? to / KT : 0);
+        }
+        return w;
     };
+    const Whole whole = whole_tiles(rt0, rt1), block_whole = KEYS ? whole : whole_tiles(0, nt - 1);
     const uint64_t *bits = nullptr;
     if constexpr (TREE) bits = a.tree + b * a.tree_stride[0] + (token - b * a.drafts) * a.tree_stride[1];
     // the tokens of a tile that the lane's row sees, `ok` the groups of 16 whose page is there
@@ -416,8 +426,10 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
         const u32x2 x = read_transposed(p), y = read_transposed(p + 8 * VSTR);
         return u32x4{x[0], x[1], y[0], y[1]};
     };
-    auto compute = [&](const char *t, int base, uint32_t ok) {
-        const bool partial = ok != (1u << NG) - 1 || !all_seen(base, rt0, rt1);
+    // `between` is work that hides behind the score products
+    auto compute = [&](const char *t, int j, uint32_t ok, auto between) {
+        const int base = tile_base(j);
+        const bool partial = ok != (1u << NG) - 1 || !whole.has(j);
         f32x16 s[NS];
 #pragma unroll
         for (int u = 0; u < NS; ++u) {
@@ -429,6 +441,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
                 s[u] = mfma32(__builtin_bit_cast(E8, w), q[i], s[u]);
             }
         }
+        between();
         const float *sc = (const float *)(t + KT * (KSTR + VSTR)) + 4 * h;
         if constexpr (Q8) {
 #pragma unroll
@@ -551,59 +564,61 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
             look_up(j + 4);
         }
         for (; j < j1; j += 4) {
-            const int base = tile_base(j);
             const uint32_t ok = there;
-            bad |= store_tile(my_lds, base, !all_seen(base, 0, nt - 1), false);
+            bad |= store_tile(my_lds, tile_base(j), !whole.has(j), false);
             own_order();
             load_tile();  // the wave's next one; past the end the last one, which is not used
             look_up(j + 8);
-            if (!none_seen(base, 0, nt - 1)) compute(my_lds, base, ok);
+            compute(my_lds, j, ok, [] {});
             own_order();
         }
         if (__any(bad))
             for (j = j0 + wave; j < j1; j += 4) {
-                const int base = tile_base(j);
-                if (all_seen(base, 0, nt - 1)) continue;
+                if (whole.has(j)) continue;
                 look_up(j);
                 load_tile();
-                store_tile(my_lds, base, true, true);
+                store_tile(my_lds, tile_base(j), true, true);
                 own_order();
-                add_kinds(my_lds, base);
+                add_kinds(my_lds, tile_base(j));
                 own_order();
             }
     } else if (j0 < j1) {
+        // the tile in the registers, j (or, past the end, the last one again), into a buffer
         auto fill = [&](int j, int buffer, bool raw) {
-            const int base = tile_base(j);
-            bad |= store_tile(lds + buffer * UNIT, base, !all_seen(base, 0, nt - 1), raw);
-            if (lane == 0) there_lds[buffer][wave] = there;
+            j = j < j1 ? j : j1 - 1;
+            bad |= store_tile(lds + buffer * UNIT, tile_base(j), !block_whole.has(j), raw);
+            if (lane == 0) ((uint8_t *)&there_lds[buffer])[wave] = (uint8_t)there;
         };
         look_up(j0);
         load_tile();
         look_up(j0 + 1);
         fill(j0, j0 & 1, false);
+        load_tile();
+        look_up(j0 + 2);
         __syncthreads();
         for (int j = j0; j < j1; ++j) {
-            const int base = tile_base(j);
-            load_tile();  // the next one; past the end the last one, which is not used
-            look_up(j + 2);
-            if (!idle && !none_seen(base, rt0, rt1)) {
-                uint32_t ok = 0;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) ok |= (uint32_t)__builtin_amdgcn_readfirstlane(there_lds[j & 1][w]) << w;
-                compute(lds + (j & 1) * UNIT, base, ok);
+            auto next = [&]() {
+                fill(j + 1, (j + 1) & 1, false);
+                load_tile();
+                look_up(j + 3);
+            };
+            if (idle) {
+                next();
+            } else {
+                // a byte for each group
+                const uint32_t ok = ((uint32_t)__builtin_amdgcn_readfirstlane(there_lds[j & 1]) * 0x01020408u) >> 24;
+                compute(lds + (j & 1) * UNIT, j, ok, next);
             }
-            if (j + 1 < j1) fill(j + 1, (j + 1) & 1, false);
             __syncthreads();
         }
         if (__syncthreads_or(bad))
             for (int j = j0; j < j1; ++j) {
-                const int base = tile_base(j);
-                if (all_seen(base, 0, nt - 1)) continue;
+                if (block_whole.has(j)) continue;
                 look_up(j);
                 load_tile();
                 fill(j, 0, true);
                 __syncthreads();
-                if (!idle) add_kinds(lds, base);
+                if (!idle) add_kinds(lds, tile_base(j));
                 __syncthreads();
             }
     }
