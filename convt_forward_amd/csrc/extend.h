@@ -47,19 +47,23 @@ struct ExtendArgs {
 };
 hipError_t launch_extend_direct(const ExtendArgs &a, int dtype, int quantised, hipStream_t stream);
 
+// The forms of the matrix-core kernel (kextend_mfma.h): few rows, whose waves
+// share the tokens, and 128 or 256 rows a block.
+enum class ExtendForm : int32_t { kKeys, kRows128, kRows256 };
+
 // How a launch's blocks of the matrix-core kernel map to the rows.
 struct ExtendTiles {
+    ExtendForm form;
     int32_t block_tokens;   // tokens of a tile of rows
     int32_t head_tiles;     // tiles of the query heads that share a kv head
     int32_t stream_tiles;   // tiles of a stream where all have the same number (trees, no starts), else 0
     int32_t tiles;          // of the grid
     FastDiv div_kv, div_head_tiles, div_stream_tiles;
 };
-// keys: the form for few rows
-hipError_t launch_extend_bf16(const ExtendArgs &a, const ExtendTiles &t, bool keys, hipStream_t stream);
-hipError_t launch_extend_f16(const ExtendArgs &a, const ExtendTiles &t, bool keys, hipStream_t stream);
-hipError_t launch_extend_bf16_q8(const ExtendArgs &a, const ExtendTiles &t, bool keys, hipStream_t stream);
-hipError_t launch_extend_f16_q8(const ExtendArgs &a, const ExtendTiles &t, bool keys, hipStream_t stream);
+hipError_t launch_extend_bf16(const ExtendArgs &a, const ExtendTiles &t, hipStream_t stream);
+hipError_t launch_extend_f16(const ExtendArgs &a, const ExtendTiles &t, hipStream_t stream);
+hipError_t launch_extend_bf16_q8(const ExtendArgs &a, const ExtendTiles &t, hipStream_t stream);
+hipError_t launch_extend_f16_q8(const ExtendArgs &a, const ExtendTiles &t, hipStream_t stream);
 hipError_t launch_extend_join(const ExtendArgs &a, int dtype, hipStream_t stream);
 
 }  // namespace convt

@@ -29,13 +29,16 @@ bool mfma_serves(const convt_cache_desc &c, const int64_t *q_stride, int n) {
 // The form of the matrix-core kernel and its tiles for streams of `each` new
 // tokens (ragged ones: on average).
 struct Shape {
-    bool keys;
+    ExtendForm form;
     int64_t block_tokens, head_tiles, stream_tiles, tiles;
 };
-Shape shape_of(int64_t batch, int64_t tokens, int64_t each, bool ragged, int64_t share) {
+Shape shape_of(int64_t batch, int64_t tokens, int64_t each, bool ragged, int64_t share, int32_t head_dim) {
     Shape s;
-    s.keys = each * share <= 32;
-    const int64_t rows = s.keys ? 32 : 128;
+    // more than 128 dims leave a SIMD the registers of one wave, 4 a block
+    s.form = each * share <= 32                      ? ExtendForm::kKeys
+             : each * share <= 128 || head_dim > 128 ? ExtendForm::kRows128
+                                                     : ExtendForm::kRows256;
+    const int64_t rows = s.form == ExtendForm::kKeys ? 32 : s.form == ExtendForm::kRows128 ? 128 : 256;
     s.block_tokens = share >= rows ? 1 : rows / share;
     s.head_tiles = ceil_div(share, rows);
     s.stream_tiles = ragged ? 0 : ceil_div(each, s.block_tokens);
@@ -61,7 +64,7 @@ convt_status extend_check(const convt_cache_desc &c, int64_t max_length, int64_t
     if (!strides_ok(q_stride, n_strides, 0) || !strides_ok(out_stride, n_strides)) return CONVT_ERR_INVALID_ARGUMENT;
     if (!isfinite(scale)) return CONVT_ERR_INVALID_ARGUMENT;
     if (route < CONVT_EXTEND_AUTO || route > CONVT_EXTEND_MFMA) return CONVT_ERR_INVALID_ARGUMENT;
-    *shape = shape_of(batch, tokens, each, ragged, heads / c.kv_heads);
+    *shape = shape_of(batch, tokens, each, ragged, heads / c.kv_heads, c.head_dim);
     const int64_t blocks = shape->tiles * shape->head_tiles * c.kv_heads;
     const bool mfma = mfma_serves(c, q_stride, n_strides) && blocks <= kMaxBlocks;
     if (route == CONVT_EXTEND_MFMA && !mfma) return CONVT_ERR_UNSUPPORTED;
@@ -72,9 +75,9 @@ convt_status extend_check(const convt_cache_desc &c, int64_t max_length, int64_t
         // a tile's rows together see what their first and last ones do, in whole tiles of 64 after
         // groups of 16, the first tokens in tiles of their own
         if (limited) longest += shape->block_tokens + 2 * 64 + 16;
-        const int64_t slots = 256 * (c.head_dim <= 128 ? 2 : 1);
+        const int64_t slots = 256 * (c.head_dim <= 128 && shape->form != ExtendForm::kRows256 ? 2 : 1);
         chunks = blocks > 0 ? slots / blocks : 1;
-        least = shape->keys ? 512 : 1024;
+        least = shape->form == ExtendForm::kKeys ? 512 : 1024;
     } else {
         chunks = rows > 0 ? 2048 / rows : 1;
         least = 2048;
@@ -154,6 +157,7 @@ convt_status launch(const ExtendArgs &a, const convt_cache_desc &c, const convt_
     hipError_t e;
     if (mfma) {
         ExtendTiles t;
+        t.form = shape.form;
         t.block_tokens = (int32_t)shape.block_tokens;
         t.head_tiles = (int32_t)shape.head_tiles;
         t.stream_tiles = (int32_t)shape.stream_tiles;
@@ -161,8 +165,8 @@ convt_status launch(const ExtendArgs &a, const convt_cache_desc &c, const convt_
         t.div_kv = divisor_of((uint32_t)a.kv_heads);
         t.div_head_tiles = divisor_of((uint32_t)t.head_tiles);
         t.div_stream_tiles = divisor_of((uint32_t)(t.stream_tiles > 0 ? t.stream_tiles : 1));
-        if (c.quantised) e = c.dtype == CONVT_DTYPE_BF16 ? launch_extend_bf16_q8(a, t, shape.keys, s) : launch_extend_f16_q8(a, t, shape.keys, s);
-        else e = c.dtype == CONVT_DTYPE_BF16 ? launch_extend_bf16(a, t, shape.keys, s) : launch_extend_f16(a, t, shape.keys, s);
+        if (c.quantised) e = c.dtype == CONVT_DTYPE_BF16 ? launch_extend_bf16_q8(a, t, s) : launch_extend_f16_q8(a, t, s);
+        else e = c.dtype == CONVT_DTYPE_BF16 ? launch_extend_bf16(a, t, s) : launch_extend_f16(a, t, s);
     } else {
         e = launch_extend_direct(a, c.dtype, c.quantised, s);
     }

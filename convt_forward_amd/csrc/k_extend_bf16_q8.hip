@@ -4,8 +4,8 @@
 
 namespace convt {
 
-hipError_t launch_extend_bf16_q8(const ExtendArgs &a, const ExtendTiles &t, bool keys, hipStream_t stream) {
-    return run_dims<__bf16, true>(a, t, keys, stream);
+hipError_t launch_extend_bf16_q8(const ExtendArgs &a, const ExtendTiles &t, hipStream_t stream) {
+    return run_dims<__bf16, true>(a, t, stream);
 }
 
 }  // namespace convt

@@ -4,8 +4,8 @@
 
 namespace convt {
 
-hipError_t launch_extend_f16(const ExtendArgs &a, const ExtendTiles &t, bool keys, hipStream_t stream) {
-    return run_dims<_Float16, false>(a, t, keys, stream);
+hipError_t launch_extend_f16(const ExtendArgs &a, const ExtendTiles &t, hipStream_t stream) {
+    return run_dims<_Float16, false>(a, t, stream);
 }
 
 }  // namespace convt

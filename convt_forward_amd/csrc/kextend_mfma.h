@@ -101,9 +101,9 @@ template <uint32_t INF, uint32_t ONE> __device__ __forceinline__ uint32_t word_k
 
 constexpr int next_pow2(int n) { return n <= 1 ? 1 : 2 * next_pow2((n + 1) / 2); }
 
-// DP: head_dim rounded up to 64, 96, 128 or 256.
-template <typename E, bool Q8, int DP, bool KEYS, bool TREE>
-__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs a, ExtendTiles tl) {
+// DP: head_dim rounded up to 64, 96, 128 or 256. WAVES: of a block, 8 only in the form for many rows.
+template <typename E, bool Q8, int DP, bool KEYS, int WAVES, bool TREE>
+__global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs a, ExtendTiles tl) {
     typedef typename std::conditional<Q8, _Float16, E>::type EV;  // P and V
     typedef typename Vec8<E>::type E8;
     typedef typename Vec8<EV>::type EV8;
@@ -112,8 +112,9 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
     constexpr uint32_t INF = __is_same(EV, __bf16) ? 0x7f80u : 0x7c00u, ONE = __is_same(EV, __bf16) ? 0x3f80u : 0x3c00u;
     constexpr int KT = KEYS ? 32 : 64;           // tokens of a tile
     constexpr int NS = KT / 32, NG = KT / 16;
-    constexpr int ROWS = KEYS ? 32 : 128;        // of a block
+    constexpr int ROWS = KEYS ? 32 : 32 * WAVES; // of a block
     constexpr int GW = KEYS ? 2 : 1;             // groups of 16 tokens that a wave fills
+    constexpr int SIDES = WAVES == 8 ? 1 : 2;    // K and V of them, or one of the two
     constexpr int CS = Q8 ? 1 : 2;               // bytes of a cache element
     constexpr int CHP = next_pow2(DP * CS / 16); // lanes along a token's row in the cache, 16 bytes each
     constexpr int RS = 64 / CHP;                 // rows they take at a time
@@ -283,27 +284,32 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
         }
     }
 
-    // ---- filling tiles: a wave takes whole groups of 16 tokens, which lie in one page
+    // ---- filling tiles: a wave takes whole groups of 16 tokens, which lie in one page; of
+    // 8 waves the first 4 take K and the others V
+    const int g0 = KEYS ? 0 : wave % 4;  // the wave's first group of a tile
+    auto is_v = [&](int side) { return SIDES == 2 ? side == 1 : wave >= 4; };
     const int r0 = lane / CHP, col = lane % CHP;
     const bool active = col * (16 / CS) < D;
-    const uint32_t k_tok = (uint32_t)a.k_stride[2] * CS, v_tok = (uint32_t)a.v_stride[2] * CS;  // bytes between tokens
-    const char *kc = (const char *)a.k_cache + kvh * a.k_stride[1] * CS, *vc = (const char *)a.v_cache + kvh * a.v_stride[1] * CS;
-    uint32_t k_lane[NCH], v_lane[NCH];  // the lane's bytes in a group (less than 2^30 by the route's rule)
+    const char *cells[SIDES];
+    uint32_t page_step[SIDES], token_step[SIDES];  // elements between pages, bytes between tokens
+    uint32_t at_lane[SIDES][NCH];                  // the lane's bytes in a group (less than 2^30 by the route's rule)
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-        k_lane[i] = (r0 + i * RS) * k_tok + (active ? col : 0) * 16;
-        v_lane[i] = (r0 + i * RS) * v_tok + (active ? col : 0) * 16;
+    for (int s = 0; s < SIDES; ++s) {
+        cells[s] = is_v(s) ? (const char *)a.v_cache + kvh * a.v_stride[1] * CS : (const char *)a.k_cache + kvh * a.k_stride[1] * CS;
+        page_step[s] = (uint32_t)(is_v(s) ? a.v_stride[0] : a.k_stride[0]);
+        token_step[s] = (uint32_t)(is_v(s) ? a.v_stride[2] : a.k_stride[2]) * CS;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) at_lane[s][i] = (r0 + i * RS) * token_step[s] + (active ? col : 0) * 16;
     }
     const int32_t *table = a.page_table + b * a.table_stride;
-    const int g0 = KEYS ? 0 : wave;  // the wave's first group of a tile
     char *my_lds = KEYS ? lds + wave * UNIT : lds;
     if (D < DP) {
         // the dims of K past D, which meet zeros of Q, are zeros; no piece is stored there
-        for (int i = threadIdx.x * 4; i < (int)sizeof(lds); i += 256 * 4) *(uint32_t *)(lds + i) = 0;
+        for (int i = threadIdx.x * 4; i < (int)sizeof(lds); i += 64 * WAVES * 4) *(uint32_t *)(lds + i) = 0;
         __syncthreads();
     }
-    u32x4 kr[GW][NCH], vr[GW][NCH];
-    float ks_r = 0.0f, vs_r = 0.0f;
+    u32x4 raw[SIDES][GW][NCH];
+    float scale_raw[SIDES] = {};
     int32_t entry[GW];
     int entry_off[GW];
     uint32_t there = 0;  // the groups of the tile in the registers whose page is there
@@ -327,84 +333,88 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
             const bool ok = entry[g] >= 0 && entry[g] < a.n_pages;
             const uint32_t page = ok ? entry[g] : 0, off = entry_off[g];
             there |= ok ? 1u << g : 0;
-            // strides of less than 2^31 elements: 32-bit factors
-            const char *kp = kc + ((uint64_t)page * (uint32_t)a.k_stride[0] * CS + (uint64_t)off * k_tok);
-            const char *vp = vc + ((uint64_t)page * (uint32_t)a.v_stride[0] * CS + (uint64_t)off * v_tok);
 #pragma unroll
-            for (int i = 0; i < NCH; ++i) {
-                kr[g][i] = *(const u32x4 *)(kp + k_lane[i]);
-                vr[g][i] = *(const u32x4 *)(vp + v_lane[i]);
-            }
-            if constexpr (Q8) {
-                const uint64_t at = (uint64_t)page * (uint32_t)(a.kv_heads * a.page_size) + (uint32_t)(kvh * a.page_size + (int)off);
-                // lanes 16 g .. of the groups' tokens; the others read what they do not use
-                const float k = a.k_scale[at + (uint32_t)(lane % 16)], v = a.v_scale[at + (uint32_t)(lane % 16)];
-                ks_r = GW == 1 || lane / 16 == g ? k : ks_r;
-                vs_r = GW == 1 || lane / 16 == g ? v : vs_r;
+            for (int s = 0; s < SIDES; ++s) {
+                // strides of less than 2^31 elements: 32-bit factors
+                const char *p = cells[s] + ((uint64_t)page * page_step[s] * CS + (uint64_t)off * token_step[s]);
+#pragma unroll
+                for (int i = 0; i < NCH; ++i) raw[s][g][i] = *(const u32x4 *)(p + at_lane[s][i]);
+                if constexpr (Q8) {
+                    const uint64_t at = (uint64_t)page * (uint32_t)(a.kv_heads * a.page_size) + (uint32_t)(kvh * a.page_size + (int)off);
+                    // lanes 16 g .. of the groups' tokens; the others read what they do not use
+                    const float v = (is_v(s) ? a.v_scale : a.k_scale)[at + (uint32_t)(lane % 16)];
+                    scale_raw[s] = GW == 1 || lane / 16 == g ? v : scale_raw[s];
+                }
             }
         }
     };
     // edge: some row of the block does not see some token. Values that no
-    // row sees become 0 then, infinities and NaN too unless `raw`; returns
+    // row sees become 0 then, infinities and NaN too unless `keep`; returns
     // whether there were any.
-    auto store_tile = [&](char *to, int base, bool edge, bool raw) {
+    auto store_tile = [&](char *to, int base, bool edge, bool keep) {
         bool bad = false;
         const bool cut = edge || there != (1u << GW) - 1;
 #pragma unroll
-        for (int g = 0; g < GW; ++g)
+        for (int s = 0; s < SIDES; ++s) {
+            constexpr int PW = Q8 ? 2 : 1;  // 16-byte words of LDS for one of the cache
+            u32x4 w[GW][NCH][PW];
 #pragma unroll
-            for (int i = 0; i < NCH; ++i) {
-                const int r = 16 * (g0 + g) + r0 + i * RS;
-                if (cut) {
-                    const bool seen = base + r <= hi && (there >> g & 1);
+            for (int g = 0; g < GW; ++g)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) vr[g][i][k] = seen ? vr[g][i][k] : 0;
-                }
-                char *kp = to + r * KSTR + col * (32 / CS), *vp = to + KT * KSTR + r * VSTR + col * (32 / CS);
-                if constexpr (Q8) {
-                    u32x4 kw[2], vw[2];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        kw[k / 2][k % 2 * 2] = e4m3_pair<E, false>(kr[g][i][k]);
-                        kw[k / 2][k % 2 * 2 + 1] = e4m3_pair<E, true>(kr[g][i][k]);
-                        vw[k / 2][k % 2 * 2] = e4m3_pair<EV, false>(vr[g][i][k]);
-                        vw[k / 2][k % 2 * 2 + 1] = e4m3_pair<EV, true>(vr[g][i][k]);
-                    }
-                    if (edge)
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint32_t w = word_finite<INF>(vw[k / 4][k % 4]);
-                            bad |= w != vw[k / 4][k % 4];
-                            vw[k / 4][k % 4] = raw ? vw[k / 4][k % 4] : w;
-                        }
-                    if (active) {
-                        *(u32x4 *)kp = kw[0];
-                        *(u32x4 *)(kp + 16) = kw[1];
-                        *(u32x4 *)vp = vw[0];
-                        *(u32x4 *)(vp + 16) = vw[1];
-                    }
-                } else {
-                    if (edge)
+                for (int i = 0; i < NCH; ++i) {
+                    if constexpr (Q8) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const uint32_t w = word_finite<INF>(vr[g][i][k]);
-                            bad |= w != vr[g][i][k];
-                            vr[g][i][k] = raw ? vr[g][i][k] : w;
+                            const uint32_t x = raw[s][g][i][k];
+                            if (is_v(s)) {
+                                w[g][i][k / 2][k % 2 * 2] = e4m3_pair<EV, false>(x);
+                                w[g][i][k / 2][k % 2 * 2 + 1] = e4m3_pair<EV, true>(x);
+                            } else {
+                                w[g][i][k / 2][k % 2 * 2] = e4m3_pair<E, false>(x);
+                                w[g][i][k / 2][k % 2 * 2 + 1] = e4m3_pair<E, true>(x);
+                            }
                         }
-                    if (active) {
-                        *(u32x4 *)kp = kr[g][i];
-                        *(u32x4 *)vp = vr[g][i];
+                    } else {
+                        w[g][i][0] = raw[s][g][i];
                     }
                 }
+            if (is_v(s) && cut) {
+#pragma unroll
+                for (int g = 0; g < GW; ++g)
+#pragma unroll
+                    for (int i = 0; i < NCH; ++i) {
+                        const bool seen = base + 16 * (g0 + g) + r0 + i * RS <= hi && (there >> g & 1);
+#pragma unroll
+                        for (int k = 0; k < 4 * PW; ++k) {
+                            const uint32_t x = seen ? w[g][i][k / 4][k % 4] : 0, f = word_finite<INF>(x);
+                            bad |= edge && f != x;
+                            w[g][i][k / 4][k % 4] = edge && !keep ? f : x;
+                        }
+                    }
             }
-        if constexpr (Q8) {
-            if (lane < 16 * GW) {
-                // a scale that is not a number leaves the sum through its score alone
-                float *s = (float *)(to + KT * (KSTR + VSTR)) + 16 * g0 + lane;
-                const float v = vs_r < 0x1p-126f ? 0x1p-126f : vs_r;
-                s[0] = ks_r * c;
-                s[KT] = log2f(v);
-                s[2 * KT] = v == v ? 1.0f / v : 0.0f;
+            if (active) {
+#pragma unroll
+                for (int g = 0; g < GW; ++g)
+#pragma unroll
+                    for (int i = 0; i < NCH; ++i) {
+                        const int r = 16 * (g0 + g) + r0 + i * RS;
+                        char *p = to + (is_v(s) ? KT * KSTR + r * VSTR : r * KSTR) + col * (16 * PW);
+#pragma unroll
+                        for (int k = 0; k < PW; ++k) *(u32x4 *)(p + 16 * k) = w[g][i][k];
+                    }
+            }
+            if constexpr (Q8) {
+                if (lane < 16 * GW) {
+                    float *sp = (float *)(to + KT * (KSTR + VSTR)) + 16 * g0 + lane;
+                    if (is_v(s)) {
+                        // a scale that is not a number leaves the sum through its score alone
+                        const float v = scale_raw[s] < 0x1p-126f ? 0x1p-126f : scale_raw[s];
+                        sp[KT] = log2f(v);
+                        sp[2 * KT] = v == v ? 1.0f / v : 0.0f;
+                    } else {
+                        sp[0] = scale_raw[s] * c;
+                    }
+                }
             }
         }
         return bad;
@@ -421,16 +431,9 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
     const int k_at = r32 * KSTR + h * 16;
     const int v_at = KT * KSTR + (4 * h + lane % 16 / 4) * VSTR + (lane / 16 % 2 * 16 + lane % 4 * 4) * 2;
 
-    auto v_word = [&](const char *t, int k, int d) {  // 8 tokens of step k of 16, a dim of tile d
-        const char *p = t + v_at + 16 * k * VSTR + d * 64;
-        const u32x2 x = read_transposed(p), y = read_transposed(p + 8 * VSTR);
-        return u32x4{x[0], x[1], y[0], y[1]};
-    };
-    // `between` is work that hides behind the score products
-    auto compute = [&](const char *t, int j, uint32_t ok, auto between) {
-        const int base = tile_base(j);
-        const bool partial = ok != (1u << NG) - 1 || !whole.has(j);
-        f32x16 s[NS];
+    f32x16 s[NS];                 // scores, then weights, of a tile
+    u32x4 ph[NS * 2], pl[NS * 2]; // the weights as the B operand: their EV value, what it leaves
+    auto scores = [&](const char *t) {
 #pragma unroll
         for (int u = 0; u < NS; ++u) {
 #pragma unroll
@@ -441,7 +444,8 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
                 s[u] = mfma32(__builtin_bit_cast(E8, w), q[i], s[u]);
             }
         }
-        between();
+    };
+    auto weights = [&](const char *t, int j, uint32_t ok) {
         const float *sc = (const float *)(t + KT * (KSTR + VSTR)) + 4 * h;
         if constexpr (Q8) {
 #pragma unroll
@@ -453,8 +457,8 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
                     for (int i = 0; i < 4; ++i) s[u][g * 4 + i] = __builtin_fmaf(s[u][g * 4 + i], k[i], v[i]);
                 }
         }
-        if (partial) {
-            const uint64_t seen = seen_bits(base, ok) >> (4 * h);
+        if (ok != (1u << NG) - 1 || !whole.has(j)) {
+            const uint64_t seen = seen_bits(tile_base(j), ok) >> (4 * h);
 #pragma unroll
             for (int u = 0; u < NS; ++u)
 #pragma unroll
@@ -498,7 +502,6 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
 #pragma unroll
                 for (int i = 0; i < 16; ++i) l += s[u][i];
         }
-        u32x4 ph[NS * 2], pl[NS * 2];
 #pragma unroll
         for (int k = 0; k < NS * 2; ++k)
 #pragma unroll
@@ -508,6 +511,13 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
                 if constexpr (SPLIT)
                     pl[k][i] = pack_half2<EV>(x - __uint_as_float(ph[k][i] << 16), y - __uint_as_float(ph[k][i] & 0xffff0000u));
             }
+    };
+    auto v_word = [&](const char *t, int k, int d) {  // 8 tokens of step k of 16, a dim of tile d
+        const char *p = t + v_at + 16 * k * VSTR + d * 64;
+        const u32x2 x = read_transposed(p), y = read_transposed(p + 8 * VSTR);
+        return u32x4{x[0], x[1], y[0], y[1]};
+    };
+    auto values = [&](const char *t) {
 #pragma unroll
         for (int k = 0; k < NS * 2; ++k)
 #pragma unroll
@@ -521,6 +531,24 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
                     o[d] = mfma32(__builtin_bit_cast(EV8, w), __builtin_bit_cast(EV8, pl[k]), o[d]);
                 }
             }
+    };
+    // The order of the LDS reads and products of values() and scores() in one phase: two groups of 4
+    // operands ahead of the products. Left alone the compiler reads two operands
+    // and waits for both.
+    auto pipeline = [&]() {
+        constexpr int GV = NS * 2 * ND / 4, GK = NS * NC / 4;
+        __builtin_amdgcn_sched_group_barrier(0x100, 16, 0);  // LDS reads, two for an operand of V
+#pragma unroll
+        for (int i = 2; i < GV; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 4, 0);  // products
+            __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < GK; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 4, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x8, 8, 0);
     };
     // Infinities and NaN of a tile that not all rows see: for each kind, whether the row sees one in the dim.
     auto add_kinds = [&](const char *t, int base) {
@@ -569,7 +597,9 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
             own_order();
             load_tile();  // the wave's next one; past the end the last one, which is not used
             look_up(j + 8);
-            compute(my_lds, j, ok, [] {});
+            scores(my_lds);
+            weights(my_lds, j, ok);
+            values(my_lds);
             own_order();
         }
         if (__any(bad))
@@ -587,29 +617,70 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
         auto fill = [&](int j, int buffer, bool raw) {
             j = j < j1 ? j : j1 - 1;
             bad |= store_tile(lds + buffer * UNIT, tile_base(j), !block_whole.has(j), raw);
-            if (lane == 0) ((uint8_t *)&there_lds[buffer])[wave] = (uint8_t)there;
+            if (lane == 0 && wave < 4) ((uint8_t *)&there_lds[buffer])[wave] = (uint8_t)there;
         };
         look_up(j0);
         load_tile();
         look_up(j0 + 1);
         fill(j0, j0 & 1, false);
-        load_tile();
-        look_up(j0 + 2);
+        if constexpr (WAVES == 4) {
+            load_tile();
+            look_up(j0 + 2);
+        }
         __syncthreads();
-        for (int j = j0; j < j1; ++j) {
-            auto next = [&]() {
-                fill(j + 1, (j + 1) & 1, false);
-                load_tile();
-                look_up(j + 3);
-            };
-            if (idle) {
-                next();
-            } else {
-                // a byte for each group
-                const uint32_t ok = ((uint32_t)__builtin_amdgcn_readfirstlane(there_lds[j & 1]) * 0x01020408u) >> 24;
-                compute(lds + (j & 1) * UNIT, j, ok, next);
+        auto next = [&](int j) {
+            fill(j + 1, (j + 1) & 1, false);
+            load_tile();
+            look_up(j + 3);
+        };
+        // a byte for each group
+        auto ok_of = [&](int j) { return ((uint32_t)__builtin_amdgcn_readfirstlane(there_lds[j & 1]) * 0x01020408u) >> 24; };
+        if constexpr (WAVES == 4) {
+            for (int j = j0; j < j1; ++j) {
+                const char *t = lds + (j & 1) * UNIT;
+                if (!idle) scores(t);
+                next(j);  // behind the products
+                if (!idle) {
+                    weights(t, j, ok_of(j));
+                    values(t);
+                }
+                __syncthreads();
             }
-            __syncthreads();
+        } else {
+            // The two waves of a SIMD take turns: while one multiplies (the values of tile j, then the
+            // scores of tile j + 1) the other forms weights and fills a buffer. With the phases
+            // counted from the first waves' scores of tile j0 and n = j - j0, these form the weights of tile j in
+            // phase 2 n + 1 and multiply in 2 n + 2, the others one phase later. Tile j + 1's buffer, filled
+            // in the phases of the weights of j, held tile j - 1, whose V is read
+            // last in phase 2 n + 1 by the others and 2 n by the first.
+            const bool second = wave >= 4;
+            if (second) __syncthreads();
+            if (idle) {
+                __syncthreads();
+                for (int j = j0; j < j1; ++j) {
+                    load_tile();
+                    look_up(j + 2);
+                    fill(j + 1, (j + 1) & 1, false);
+                    __syncthreads();
+                    __syncthreads();
+                }
+            } else {
+                load_tile();
+                scores(lds + (j0 & 1) * UNIT);
+                __syncthreads();
+                for (int j = j0; j < j1; ++j) {
+                    look_up(j + 2);
+                    weights(lds + (j & 1) * UNIT, j, ok_of(j));
+                    fill(j + 1, (j + 1) & 1, false);
+                    __syncthreads();
+                    load_tile();  // of j + 2, behind the products
+                    values(lds + (j & 1) * UNIT);
+                    scores(lds + ((j + 1) & 1) * UNIT);  // past the end of the last tile again, which is not used
+                    pipeline();
+                    __syncthreads();
+                }
+            }
+            if (!second) __syncthreads();
         }
         if (__syncthreads_or(bad))
             for (int j = j0; j < j1; ++j) {
@@ -696,22 +767,23 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs
     }
 }
 
-template <typename E, bool Q8, int DP> void run_extend(const ExtendArgs &a, const ExtendTiles &t, bool keys, hipStream_t s) {
+template <typename E, bool Q8, int DP, bool TREE> void run_form(const ExtendArgs &a, const ExtendTiles &t, hipStream_t s) {
     const dim3 grid((unsigned)t.tiles * (unsigned)t.head_tiles * (unsigned)a.kv_heads, (unsigned)a.chunks);
-    if (a.tree) {
-        if (keys) extend_mfma<E, Q8, DP, true, true><<<grid, 256, 0, s>>>(a, t);
-        else extend_mfma<E, Q8, DP, false, true><<<grid, 256, 0, s>>>(a, t);
-    } else {
-        if (keys) extend_mfma<E, Q8, DP, true, false><<<grid, 256, 0, s>>>(a, t);
-        else extend_mfma<E, Q8, DP, false, false><<<grid, 256, 0, s>>>(a, t);
-    }
+    if (t.form == ExtendForm::kKeys) extend_mfma<E, Q8, DP, true, 4, TREE><<<grid, 256, 0, s>>>(a, t);
+    else if (t.form == ExtendForm::kRows128) extend_mfma<E, Q8, DP, false, 4, TREE><<<grid, 256, 0, s>>>(a, t);
+    else if constexpr (DP <= 128) extend_mfma<E, Q8, DP, false, 8, TREE><<<grid, 512, 0, s>>>(a, t);
 }
 
-template <typename E, bool Q8> hipError_t run_dims(const ExtendArgs &a, const ExtendTiles &t, bool keys, hipStream_t s) {
-    if (a.head_dim <= 64) run_extend<E, Q8, 64>(a, t, keys, s);
-    else if (a.head_dim <= 96) run_extend<E, Q8, 96>(a, t, keys, s);
-    else if (a.head_dim <= 128) run_extend<E, Q8, 128>(a, t, keys, s);
-    else run_extend<E, Q8, 256>(a, t, keys, s);
+template <typename E, bool Q8, int DP> void run_extend(const ExtendArgs &a, const ExtendTiles &t, hipStream_t s) {
+    if (a.tree) run_form<E, Q8, DP, true>(a, t, s);
+    else run_form<E, Q8, DP, false>(a, t, s);
+}
+
+template <typename E, bool Q8> hipError_t run_dims(const ExtendArgs &a, const ExtendTiles &t, hipStream_t s) {
+    if (a.head_dim <= 64) run_extend<E, Q8, 64>(a, t, s);
+    else if (a.head_dim <= 96) run_extend<E, Q8, 96>(a, t, s);
+    else if (a.head_dim <= 128) run_extend<E, Q8, 128>(a, t, s);
+    else run_extend<E, Q8, 256>(a, t, s);
     return hipGetLastError();
 }
 
