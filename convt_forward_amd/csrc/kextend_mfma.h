@@ -88,6 +88,12 @@ template <uint32_t INF> __device__ __forceinline__ uint32_t word_finite(uint32_t
     const uint32_t lo = (w & INF) == INF ? 0 : w & 0xffffu, hi = (w & (INF << 16)) == INF << 16 ? 0 : w & 0xffff0000u;
     return lo | hi;
 }
+// Four e4m3 codes with NaN, 0x7f of either sign, replaced by 0.
+__device__ __forceinline__ uint32_t codes_finite(uint32_t w) {
+    uint32_t r = 0;
+    for (int i = 0; i < 4; ++i) r |= (w >> (8 * i) & 0x7f) == 0x7f ? 0 : w & 0xffu << (8 * i);
+    return r;
+}
 // 1 (ONE its bits) where a value is of the kind: 0 infinity, 1 -infinity, 2 NaN.
 template <uint32_t INF, uint32_t ONE> __device__ __forceinline__ uint32_t word_kind(uint32_t w, int kind) {
     uint32_t r = 0;
@@ -121,10 +127,12 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
     constexpr int NCH = 16 / RS;                 // pieces of a lane in a group
     constexpr int KSTR = DP * 2 + 16, VSTR = DP == 96 ? 192 : DP * 2 + 64;  // bytes between tokens in LDS
     constexpr int UNIT = KT * (KSTR + VSTR) + (Q8 ? 3 * KT * 4 : 0);
+    constexpr int BUFFERS = WAVES == 8 ? 3 : 2;  // of tiles, in the form for many rows
     constexpr int NC = DP / 16, ND = DP / 32;
-    __shared__ __attribute__((aligned(16))) char lds[(KEYS ? 4 : 2) * UNIT];
+    constexpr int AHEAD = WAVES == 8 ? 8 : 0;    // operands of V that are read before the products' phase
+    __shared__ __attribute__((aligned(16))) char lds[(KEYS ? 4 : BUFFERS) * UNIT];
     __shared__ float m_lds[4][32], l_lds[4][32];
-    __shared__ int there_lds[2];  // whether a tile's groups have pages, a byte each
+    __shared__ int there_lds[BUFFERS];  // whether a tile's groups have pages, a byte each
 
     const int lane = threadIdx.x % 64, r32 = lane % 32, h = lane / 32;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -348,61 +356,63 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
             }
         }
     };
-    // edge: some row of the block does not see some token. Values that no
-    // row sees become 0 then, infinities and NaN too unless `keep`; returns
-    // whether there were any.
-    auto store_tile = [&](char *to, int base, bool edge, bool keep) {
+    // Where some row of the block does not see some token of the tile in the registers (edge), values that no row
+    // sees become 0, infinities and NaN too unless `keep`. Returns whether there were any.
+    auto clean_tile = [&](int base, bool edge, bool keep) {
         bool bad = false;
-        const bool cut = edge || there != (1u << GW) - 1;
+        if (edge || there != (1u << GW) - 1) {
 #pragma unroll
-        for (int s = 0; s < SIDES; ++s) {
-            constexpr int PW = Q8 ? 2 : 1;  // 16-byte words of LDS for one of the cache
-            u32x4 w[GW][NCH][PW];
-#pragma unroll
-            for (int g = 0; g < GW; ++g)
-#pragma unroll
-                for (int i = 0; i < NCH; ++i) {
-                    if constexpr (Q8) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t x = raw[s][g][i][k];
-                            if (is_v(s)) {
-                                w[g][i][k / 2][k % 2 * 2] = e4m3_pair<EV, false>(x);
-                                w[g][i][k / 2][k % 2 * 2 + 1] = e4m3_pair<EV, true>(x);
-                            } else {
-                                w[g][i][k / 2][k % 2 * 2] = e4m3_pair<E, false>(x);
-                                w[g][i][k / 2][k % 2 * 2 + 1] = e4m3_pair<E, true>(x);
-                            }
-                        }
-                    } else {
-                        w[g][i][0] = raw[s][g][i];
-                    }
-                }
-            if (is_v(s) && cut) {
+            for (int s = 0; s < SIDES; ++s) {
+                if (!is_v(s)) continue;
 #pragma unroll
                 for (int g = 0; g < GW; ++g)
 #pragma unroll
                     for (int i = 0; i < NCH; ++i) {
                         const bool seen = base + 16 * (g0 + g) + r0 + i * RS <= hi && (there >> g & 1);
 #pragma unroll
-                        for (int k = 0; k < 4 * PW; ++k) {
-                            const uint32_t x = seen ? w[g][i][k / 4][k % 4] : 0, f = word_finite<INF>(x);
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t x = seen ? raw[s][g][i][k] : 0, f = Q8 ? codes_finite(x) : word_finite<INF>(x);
                             bad |= edge && f != x;
-                            w[g][i][k / 4][k % 4] = edge && !keep ? f : x;
+                            raw[s][g][i][k] = edge && !keep ? f : x;
                         }
                     }
             }
-            if (active) {
+        }
+        return bad;
+    };
+    auto store_tile = [&](char *to) {
 #pragma unroll
-                for (int g = 0; g < GW; ++g)
+        for (int s = 0; s < SIDES; ++s) {
+            constexpr int PW = Q8 ? 2 : 1;  // 16-byte words of LDS for one of the cache
 #pragma unroll
-                    for (int i = 0; i < NCH; ++i) {
-                        const int r = 16 * (g0 + g) + r0 + i * RS;
-                        char *p = to + (is_v(s) ? KT * KSTR + r * VSTR : r * KSTR) + col * (16 * PW);
+            for (int g = 0; g < GW; ++g)
 #pragma unroll
-                        for (int k = 0; k < PW; ++k) *(u32x4 *)(p + 16 * k) = w[g][i][k];
+                for (int i = 0; i < NCH; ++i) {
+                    u32x4 w[PW];
+                    if constexpr (Q8) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t x = raw[s][g][i][k];
+                            uint32_t lo, hi2;
+                            if constexpr (__is_same(E, EV)) {
+                                lo = e4m3_pair<E, false>(x);
+                                hi2 = e4m3_pair<E, true>(x);
+                            } else {
+                                lo = is_v(s) ? e4m3_pair<EV, false>(x) : e4m3_pair<E, false>(x);
+                                hi2 = is_v(s) ? e4m3_pair<EV, true>(x) : e4m3_pair<E, true>(x);
+                            }
+                            w[k / 2][k % 2 * 2] = lo;
+                            w[k / 2][k % 2 * 2 + 1] = hi2;
+                        }
+                    } else {
+                        w[0] = raw[s][g][i];
                     }
-            }
+                    const int r = 16 * (g0 + g) + r0 + i * RS;
+                    char *p = to + (is_v(s) ? KT * KSTR + r * VSTR : r * KSTR) + col * (16 * PW);
+                    if (active)
+#pragma unroll
+                        for (int k = 0; k < PW; ++k) *(u32x4 *)(p + 16 * k) = w[k];
+                }
             if constexpr (Q8) {
                 if (lane < 16 * GW) {
                     float *sp = (float *)(to + KT * (KSTR + VSTR)) + 16 * g0 + lane;
@@ -417,7 +427,6 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                 }
             }
         }
-        return bad;
     };
 
     f32x16 o[ND];
@@ -517,12 +526,19 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
         const u32x2 x = read_transposed(p), y = read_transposed(p + 8 * VSTR);
         return u32x4{x[0], x[1], y[0], y[1]};
     };
+    u32x4 ahead[AHEAD > 0 ? AHEAD : 1];
+    auto read_ahead = [&](const char *t) {
+#pragma unroll
+        for (int f = 0; f < AHEAD; ++f) ahead[f] = v_word(t, f / ND, f % ND);
+    };
     auto values = [&](const char *t) {
 #pragma unroll
         for (int k = 0; k < NS * 2; ++k)
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                u32x4 w = v_word(t, k, d);
+                u32x4 w;
+                if (k * ND + d < AHEAD) w = ahead[k * ND + d];
+                else w = v_word(t, k, d);
                 o[d] = mfma32(__builtin_bit_cast(EV8, w), __builtin_bit_cast(EV8, ph[k]), o[d]);
                 if constexpr (SPLIT) {
                     // the low part may be 0 or negative: an infinite value takes part in the first product only
@@ -532,23 +548,41 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                 }
             }
     };
-    // The order of the LDS reads and products of values() and scores() in one phase: two groups of 4
-    // operands ahead of the products. Left alone the compiler reads two operands
-    // and waits for both.
-    auto pipeline = [&]() {
-        constexpr int GV = NS * 2 * ND / 4, GK = NS * NC / 4;
-        __builtin_amdgcn_sched_group_barrier(0x100, 16, 0);  // LDS reads, two for an operand of V
+    // The order of a phase's LDS reads and products: operands are read two groups of 4 ahead of their
+    // products. Left alone the compiler reads two operands and waits for both: 1570
+    // cycles for the products of a tile of 64 tokens and 128 dims, 1290 so.
+    constexpr int GV = NS * 2 * ND / 4, GK = NS * NC / 4;
+    constexpr int READ = 0x100, PRODUCT = 0x8;  // LDS reads (two for an operand of V) and matrix instructions
+    auto order_scores = [&]() {
+        __builtin_amdgcn_sched_group_barrier(READ, GK > 1 ? 8 : 4, 0);
+#pragma unroll
+        for (int i = 2; i < GK; ++i) {
+            __builtin_amdgcn_sched_group_barrier(PRODUCT, 4, 0);
+            __builtin_amdgcn_sched_group_barrier(READ, 4, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(PRODUCT, GK > 1 ? 8 : 4, 0);
+    };
+    auto order_values = [&]() {
+        __builtin_amdgcn_sched_group_barrier(READ, GV > 1 ? 16 : 8, 0);
 #pragma unroll
         for (int i = 2; i < GV; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x8, 4, 0);  // products
-            __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+            __builtin_amdgcn_sched_group_barrier(PRODUCT, 4, 0);
+            __builtin_amdgcn_sched_group_barrier(READ, 8, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(PRODUCT, GV > 1 ? 8 : 4, 0);
+    };
+    auto order_both = [&]() {  // values() of a tile whose first operands are there, then scores() of another
+#pragma unroll
+        for (int i = 2; i < GV; ++i) {
+            __builtin_amdgcn_sched_group_barrier(READ, 8, 0);
+            __builtin_amdgcn_sched_group_barrier(PRODUCT, 4, 0);
         }
 #pragma unroll
         for (int i = 0; i < GK; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x8, 4, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+            __builtin_amdgcn_sched_group_barrier(READ, 4, 0);
+            __builtin_amdgcn_sched_group_barrier(PRODUCT, 4, 0);
         }
-        __builtin_amdgcn_sched_group_barrier(0x8, 8, 0);
+        __builtin_amdgcn_sched_group_barrier(PRODUCT, 8, 0);
     };
     // Infinities and NaN of a tile that not all rows see: for each kind, whether the row sees one in the dim.
     auto add_kinds = [&](const char *t, int base) {
@@ -593,13 +627,16 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
         }
         for (; j < j1; j += 4) {
             const uint32_t ok = there;
-            bad |= store_tile(my_lds, tile_base(j), !whole.has(j), false);
+            bad |= clean_tile(tile_base(j), !whole.has(j), false);
+            store_tile(my_lds);
             own_order();
             load_tile();  // the wave's next one; past the end the last one, which is not used
             look_up(j + 8);
             scores(my_lds);
+            order_scores();
             weights(my_lds, j, ok);
             values(my_lds);
+            order_values();
             own_order();
         }
         if (__any(bad))
@@ -607,77 +644,117 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                 if (whole.has(j)) continue;
                 look_up(j);
                 load_tile();
-                store_tile(my_lds, tile_base(j), true, true);
+                clean_tile(tile_base(j), true, true);
+                store_tile(my_lds);
                 own_order();
                 add_kinds(my_lds, tile_base(j));
                 own_order();
             }
     } else if (j0 < j1) {
-        // the tile in the registers, j (or, past the end, the last one again), into a buffer
-        auto fill = [&](int j, int buffer, bool raw) {
+        // Tile j, which is in the registers (past the end the last one again).
+        auto clean = [&](int j, bool keep) {
             j = j < j1 ? j : j1 - 1;
-            bad |= store_tile(lds + buffer * UNIT, tile_base(j), !block_whole.has(j), raw);
-            if (lane == 0 && wave < 4) ((uint8_t *)&there_lds[buffer])[wave] = (uint8_t)there;
+            bad |= clean_tile(tile_base(j), !block_whole.has(j), keep);
+        };
+        auto store = [&](int buffer, bool flags) {
+            store_tile(lds + buffer * UNIT);
+            if (flags && lane == 0 && wave < 4) ((uint8_t *)&there_lds[buffer])[wave] = (uint8_t)there;
         };
         look_up(j0);
         load_tile();
         look_up(j0 + 1);
-        fill(j0, j0 & 1, false);
-        if constexpr (WAVES == 4) {
-            load_tile();
-            look_up(j0 + 2);
+        // whether any page of the block's tiles is outside the cache: only then tiles have flags
+        bool outside = false;
+        {
+            const int t0 = tile_base(j0 < sink_tiles ? sink_tiles : j0), t1 = tile_base(j1 - 1) + KT - 1;
+            const int last_page = (int)fast_div((uint32_t)(t1 < hi ? t1 : hi), a.div_page);
+            for (int p = (int)fast_div((uint32_t)t0, a.div_page) + (int)threadIdx.x; p <= last_page; p += 64 * WAVES)
+                outside |= table[p] < 0 || table[p] >= a.n_pages;
+            for (int j = j0; j < sink_tiles; ++j)
+                for (int g = (int)threadIdx.x; g < NG; g += 64 * WAVES) {
+                    const int p = (int)fast_div((uint32_t)(j * KT + 16 * g < hi ? j * KT + 16 * g : hi), a.div_page);
+                    outside |= table[p] < 0 || table[p] >= a.n_pages;
+                }
         }
-        __syncthreads();
-        auto next = [&](int j) {
-            fill(j + 1, (j + 1) & 1, false);
-            load_tile();
-            look_up(j + 3);
+        clean(j0, false);
+        store(0, true);
+        load_tile();
+        look_up(j0 + 2);
+        const bool flags = __syncthreads_or(outside);
+        // the groups of a tile that have pages, from a byte for each
+        auto ok_of = [&](int buffer) {
+            uint32_t ok = (1u << NG) - 1;
+            if (flags) ok = ((uint32_t)__builtin_amdgcn_readfirstlane(there_lds[buffer]) * 0x01020408u) >> 24;
+            return ok;
         };
-        // a byte for each group
-        auto ok_of = [&](int j) { return ((uint32_t)__builtin_amdgcn_readfirstlane(there_lds[j & 1]) * 0x01020408u) >> 24; };
+        int at = 0;  // the buffer of tile j
         if constexpr (WAVES == 4) {
-            for (int j = j0; j < j1; ++j) {
-                const char *t = lds + (j & 1) * UNIT;
-                if (!idle) scores(t);
-                next(j);  // behind the products
+            for (int j = j0; j < j1; ++j, at ^= 1) {
+                const char *t = lds + at * UNIT;
                 if (!idle) {
-                    weights(t, j, ok_of(j));
+                    scores(t);
+                    order_scores();
+                }
+                // behind the products
+                clean(j + 1, false);
+                store(at ^ 1, flags);
+                load_tile();
+                look_up(j + 3);
+                if (!idle) {
+                    weights(t, j, ok_of(at));
                     values(t);
+                    order_values();
                 }
                 __syncthreads();
             }
         } else {
             // The two waves of a SIMD take turns: while one multiplies (the values of tile j, then the
-            // scores of tile j + 1) the other forms weights and fills a buffer. With the phases
-            // counted from the first waves' scores of tile j0 and n = j - j0, these form the weights of tile j in
-            // phase 2 n + 1 and multiply in 2 n + 2, the others one phase later. Tile j + 1's buffer, filled
-            // in the phases of the weights of j, held tile j - 1, whose V is read
-            // last in phase 2 n + 1 by the others and 2 n by the first.
+            // scores of tile j + 1) the other forms weights. Phases, counted from the first waves'
+            // scores of tile j0, with n = j - j0: these form the weights of tile j in phase 2 n + 1 and
+            // multiply in 2 n + 2, the others one phase later. The phase that multiplies
+            // for tile j also fills tile j + 2's buffer, of three: tile j - 1 was in it, whose values
+            // the others read last in phase 2 n + 1. Tile j + 2 is first read in phase 2 n + 4.
+            auto next = [&](int b, int by) { return b + by < 3 ? b + by : b + by - 3; };
             const bool second = wave >= 4;
             if (second) __syncthreads();
             if (idle) {
+                clean(j0 + 1, false);
+                store(1, flags);
+                load_tile();
                 __syncthreads();
                 for (int j = j0; j < j1; ++j) {
+                    look_up(j + 3);
+                    clean(j + 2, false);
+                    __syncthreads();
+                    store(next(at, 2), flags);
                     load_tile();
-                    look_up(j + 2);
-                    fill(j + 1, (j + 1) & 1, false);
                     __syncthreads();
-                    __syncthreads();
+                    at = next(at, 1);
                 }
             } else {
+                scores(lds);
+                clean(j0 + 1, false);
+                store(1, flags);
                 load_tile();
-                scores(lds + (j0 & 1) * UNIT);
                 __syncthreads();
                 for (int j = j0; j < j1; ++j) {
-                    look_up(j + 2);
-                    weights(lds + (j & 1) * UNIT, j, ok_of(j));
-                    fill(j + 1, (j + 1) & 1, false);
+                    const char *t = lds + at * UNIT;
+                    look_up(j + 3);
+                    weights(t, j, ok_of(at));
+                    // in this phase: the compiler would move them to where they are used, behind the barrier
+#pragma unroll
+                    for (int k = 0; k < NS * 2; ++k) asm volatile("" : "+v"(ph[k]));
+                    asm volatile("" : "+v"(l));
+                    read_ahead(t);
+                    clean(j + 2, false);
                     __syncthreads();
-                    load_tile();  // of j + 2, behind the products
-                    values(lds + (j & 1) * UNIT);
-                    scores(lds + ((j + 1) & 1) * UNIT);  // past the end of the last tile again, which is not used
-                    pipeline();
+                    store(next(at, 2), flags);
+                    load_tile();  // of j + 3
+                    values(t);
+                    scores(lds + next(at, 1) * UNIT);  // past the end of the last tile again, which is not used
+                    order_both();
                     __syncthreads();
+                    at = next(at, 1);
                 }
             }
             if (!second) __syncthreads();
@@ -687,7 +764,8 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                 if (block_whole.has(j)) continue;
                 look_up(j);
                 load_tile();
-                fill(j, 0, true);
+                clean(j, true);
+                store(0, false);
                 __syncthreads();
                 if (!idle) add_kinds(lds, tile_base(j));
                 __syncthreads();
