@@ -31,7 +31,10 @@ struct ExtendArgs {
     const uint64_t *tree;         // tree: not NULL
     void *out;
     float *lse;
-    float *part_o, *part_ml;      // workspace: [tokens * heads][chunks][head_dim], [..][chunks][2]
+    // workspace: [tokens * heads][chunks][head_dim], [..][chunks][2], [..]: the row's parts,
+    // 0 for a row that is done without them
+    float *part_o, *part_ml;
+    int32_t *part_count;
     int64_t q_stride[3], out_stride[3];  // batch (tree), token, head
     int64_t k_stride[3], v_stride[3];
     int64_t tree_stride[2];
@@ -41,7 +44,7 @@ struct ExtendArgs {
     int32_t heads, kv_heads, share;  // share = heads / kv_heads
     int32_t head_dim, page_size, max_length;
     int32_t window, sinks;        // window 0: no limit
-    int32_t chunks, chunk_tokens;
+    int32_t chunks, chunk_tokens;  // parts at most; tokens of one in the direct kernel
     float scale_log2e;            // scale * log2(e): the softmax runs on powers of two
     FastDiv div_page, div_heads, div_drafts;
 };
@@ -58,7 +61,9 @@ struct ExtendTiles {
     int32_t head_tiles;     // tiles of the query heads that share a kv head
     int32_t stream_tiles;   // tiles of a stream where all have the same number (trees, no starts), else 0
     int32_t tiles;          // of the grid
-    FastDiv div_kv, div_head_tiles, div_stream_tiles;
+    int32_t slots;          // blocks that the card holds at once
+    int32_t least;          // tokens that a part has at least
+    FastDiv div_kv, div_head_tiles, div_tiles, div_stream_tiles;
 };
 hipError_t launch_extend_bf16(const ExtendArgs &a, const ExtendTiles &t, hipStream_t stream);
 hipError_t launch_extend_f16(const ExtendArgs &a, const ExtendTiles &t, hipStream_t stream);

@@ -31,20 +31,36 @@ bool mfma_serves(const convt_cache_desc &c, const int64_t *q_stride, int n) {
 struct Shape {
     ExtendForm form;
     int64_t block_tokens, head_tiles, stream_tiles, tiles;
+    int64_t slots, least;  // blocks that the card holds at once, tokens of a part at least
 };
-Shape shape_of(int64_t batch, int64_t tokens, int64_t each, bool ragged, int64_t share, int32_t head_dim) {
+Shape shape_of(ExtendForm form, int64_t batch, int64_t tokens, int64_t each, bool ragged, int64_t share, int32_t head_dim) {
     Shape s;
-    // more than 128 dims leave a SIMD the registers of one wave, 4 a block
-    s.form = each * share <= 32                      ? ExtendForm::kKeys
-             : each * share <= 128 || head_dim > 128 ? ExtendForm::kRows128
-                                                     : ExtendForm::kRows256;
-    const int64_t rows = s.form == ExtendForm::kKeys ? 32 : s.form == ExtendForm::kRows128 ? 128 : 256;
+    s.form = form;
+    const int64_t rows = form == ExtendForm::kKeys ? 32 : form == ExtendForm::kRows128 ? 128 : 256;
     s.block_tokens = share >= rows ? 1 : rows / share;
     s.head_tiles = ceil_div(share, rows);
     s.stream_tiles = ragged ? 0 : ceil_div(each, s.block_tokens);
     // ragged: every stream with rows may end in a tile of its own
     s.tiles = ragged ? tokens / s.block_tokens + (batch < tokens ? batch : tokens) : batch * s.stream_tiles;
+    s.slots = 256 * (head_dim <= 128 && form != ExtendForm::kRows256 ? 2 : 1);
+    s.least = form == ExtendForm::kKeys ? 256 : 512;
     return s;
+}
+// Rows of a stream that fit in 32 share their tokens among a block's waves; more go 128 or 256 to a block
+// (above 128 dims 128: a SIMD has the registers of one wave then, 4 a block). 256 rows a block are faster
+// where blocks fill the card twice, or will do once the axis is cut, since it is long
+// against the new tokens; else the card's last blocks take too long. Measured, us, 128 and 256 rows, 32 / 8 heads of
+// 128, bf16: prompts of 512: 22, 27; 2048: 68, 66; 4096: 179, 155; 5 ragged chunks of 500 to 1000 in a
+// window of 513 (20 / 4 heads of 96): 53, 62; trees of 64 drafts over 2 x 131 K: 358, 320; 512 new ones of 16384: 174, 152.
+Shape pick_shape(int64_t batch, int64_t tokens, int64_t each, bool ragged, int64_t heads, int64_t kv_heads, int32_t head_dim, int64_t longest) {
+    const int64_t share = heads / kv_heads;
+    if (each * share <= 32) return shape_of(ExtendForm::kKeys, batch, tokens, each, ragged, share, head_dim);
+    if (each * share > 128 && head_dim <= 128) {
+        const Shape s = shape_of(ExtendForm::kRows256, batch, tokens, each, ragged, share, head_dim);
+        const int64_t blocks = s.tiles * s.head_tiles * kv_heads;
+        if (blocks >= 2 * s.slots || (longest / 4 >= each && blocks * (longest / s.least) >= s.slots)) return s;
+    }
+    return shape_of(ExtendForm::kRows128, batch, tokens, each, ragged, share, head_dim);
 }
 
 // What window and tree problems are checked for alike, and the info of one
@@ -64,7 +80,7 @@ convt_status extend_check(const convt_cache_desc &c, int64_t max_length, int64_t
     if (!strides_ok(q_stride, n_strides, 0) || !strides_ok(out_stride, n_strides)) return CONVT_ERR_INVALID_ARGUMENT;
     if (!isfinite(scale)) return CONVT_ERR_INVALID_ARGUMENT;
     if (route < CONVT_EXTEND_AUTO || route > CONVT_EXTEND_MFMA) return CONVT_ERR_INVALID_ARGUMENT;
-    *shape = shape_of(batch, tokens, each, ragged, heads / c.kv_heads, c.head_dim);
+    *shape = pick_shape(batch, tokens, each, ragged, heads, c.kv_heads, c.head_dim, longest);
     const int64_t blocks = shape->tiles * shape->head_tiles * c.kv_heads;
     const bool mfma = mfma_serves(c, q_stride, n_strides) && blocks <= kMaxBlocks;
     if (route == CONVT_EXTEND_MFMA && !mfma) return CONVT_ERR_UNSUPPORTED;
@@ -72,23 +88,27 @@ convt_status extend_check(const convt_cache_desc &c, int64_t max_length, int64_t
     const int64_t rows = tokens * heads;
     int64_t chunks, least;
     if (info->route == CONVT_EXTEND_MFMA) {
-        // a tile's rows together see what their first and last ones do, in whole tiles of 64 after
-        // groups of 16, the first tokens in tiles of their own
-        if (limited) longest += shape->block_tokens + 2 * 64 + 16;
-        const int64_t slots = 256 * (c.head_dim <= 128 && shape->form != ExtendForm::kRows256 ? 2 : 1);
-        chunks = blocks > 0 ? slots / blocks : 1;
-        least = shape->form == ExtendForm::kKeys ? 512 : 1024;
+        // Parts at most: the kernel takes as many of them as the streams' real lengths make worth while, so
+        // that the card is full once. Without a window streams may differ: up to three times as many parts
+        // for the long ones. Blocks that fill the card twice need none. Measured, us (1, 2, 3, 4, 6, 8
+        // parts): 16 ragged streams up to 4096, 25 drafts: 134, 80, 72, 62, 51, 64; 4 of 2100 to 8000, 512
+        // new tokens: 277, 265, 227, 254, 257, 258; 64 in a window of 4096, one new token: 110, 117, 122, 126, 133, 141.
+        if (blocks == 0 || blocks >= 2 * shape->slots) chunks = 1;
+        else if (limited) chunks = shape->slots / blocks;
+        else chunks = ceil_div((batch < 3 ? batch : 3) * shape->slots, blocks);
+        least = shape->least;
     } else {
         chunks = rows > 0 ? 2048 / rows : 1;
         least = 2048;
     }
     if (chunks > longest / least) chunks = longest / least;
+    if (blocks > 0 && chunks > kMaxBlocks / blocks) chunks = kMaxBlocks / blocks;
     if (chunks < 1) chunks = 1;
     const int64_t chunk = ceil_div(ceil_div(longest > 0 ? longest : 1, chunks), 64) * 64;
     chunks = longest > 0 ? ceil_div(longest, chunk) : 1;
     info->chunks = (int32_t)chunks;
     info->chunk_tokens = (int32_t)chunk;
-    info->workspace_bytes = chunks > 1 ? rows * chunks * (c.head_dim + 2) * (int64_t)sizeof(float) : 0;
+    info->workspace_bytes = chunks > 1 ? rows * (chunks * (c.head_dim + 2) + 1) * (int64_t)sizeof(float) : 0;
     info->reserved = 0;
     return CONVT_OK;
 }
@@ -130,6 +150,7 @@ ExtendArgs common_args(const convt_cache_desc &c, const convt_extend_info &info,
     a.lse = lse;
     a.part_o = (float *)workspace;
     a.part_ml = (float *)workspace + tokens * heads * info.chunks * c.head_dim;
+    a.part_count = (int32_t *)((float *)workspace + tokens * heads * info.chunks * (c.head_dim + 2));
     for (int i = 0; i < 3; ++i) {
         a.k_stride[i] = c.k_stride[i];
         a.v_stride[i] = c.v_stride[i];
@@ -162,7 +183,10 @@ convt_status launch(const ExtendArgs &a, const convt_cache_desc &c, const convt_
         t.head_tiles = (int32_t)shape.head_tiles;
         t.stream_tiles = (int32_t)shape.stream_tiles;
         t.tiles = (int32_t)shape.tiles;
+        t.slots = (int32_t)shape.slots;
+        t.least = (int32_t)shape.least;
         t.div_kv = divisor_of((uint32_t)a.kv_heads);
+        t.div_tiles = divisor_of((uint32_t)t.tiles);
         t.div_head_tiles = divisor_of((uint32_t)t.head_tiles);
         t.div_stream_tiles = divisor_of((uint32_t)(t.stream_tiles > 0 ? t.stream_tiles : 1));
         if (c.quantised) e = c.dtype == CONVT_DTYPE_BF16 ? launch_extend_bf16_q8(a, t, s) : launch_extend_f16_q8(a, t, s);

@@ -62,13 +62,8 @@ __global__ __launch_bounds__(64 * kWaves) void extend_direct(ExtendArgs a) {
     }
     const int64_t part = (int64_t)blockIdx.x * a.chunks + chunk;
     const int v0 = chunk * a.chunk_tokens;
-    if (v0 >= n && chunk > 0) {
-        if (threadIdx.x == 0) {
-            a.part_ml[part * 2] = -INFINITY;
-            a.part_ml[part * 2 + 1] = 0.0f;
-        }
-        return;
-    }
+    if (a.chunks > 1 && chunk == 0 && threadIdx.x == 0) a.part_count[blockIdx.x] = n > 0 ? (n - 1) / a.chunk_tokens + 1 : 1;
+    if (v0 >= n && chunk > 0) return;  // the join knows how many parts there are
     const int v1 = n - v0 < a.chunk_tokens ? n : v0 + a.chunk_tokens;
 
     const T *q = (const T *)a.q + q_at + h * a.q_stride[2];
@@ -193,7 +188,8 @@ __global__ __launch_bounds__(256) void extend_join(ExtendArgs a, int lanes_log2)
         real = real && (!a.starts || (token >= a.starts[0] && token < a.starts[a.batch]));
         out_at = token * a.out_stride[1];
     }
-    const int D = a.head_dim, n = real ? a.chunks : 0;
+    const int D = a.head_dim, n = real ? a.part_count[row] : 0;
+    real = n > 0;
     const float *ml = a.part_ml + (int64_t)row * a.chunks * 2;
     float m = -INFINITY;
     for (int c = tid; c < n; c += PER) m = fmaxf(m, ml[2 * c]);

@@ -107,6 +107,36 @@ template <uint32_t INF, uint32_t ONE> __device__ __forceinline__ uint32_t word_k
 
 constexpr int next_pow2(int n) { return n <= 1 ? 1 : 2 * next_pow2((n + 1) / 2); }
 
+// The tiles that a part of the axis should have: all streams' tiles shared among the blocks that the card
+// holds (tl.slots), so that ragged streams, whose lengths only the device knows, give it as
+// many blocks as equal ones; tl.least at least. Unequal parts do not come out even on all
+// shader engines, and one block too many takes as long as all: they get 0.85 of the
+// card (trees of 25 drafts over 16 ragged streams: 56 us, 64 with all of it). Where the rows alone nearly fill it,
+// unequal streams are cut into smaller parts, so that the long ones end with the others
+// (4 chunks of 512 new tokens over 2100 to 8000: 235 us, uncut 293). All blocks form the same number.
+template <int KT> __device__ __forceinline__ float part_tiles(const ExtendArgs &a, const ExtendTiles &tl, int lane) {
+    float sum = 0.0f, count = 0.0f, most = 0.0f;  // of the tiles that the last rows of each stream see, for each of its tiles of rows
+    for (int b = lane; b < a.batch; b += 64) {
+        int seen = cut_length(a, b), rows = tl.stream_tiles;
+        if (a.window > 0 && seen - a.sinks > a.window) seen = a.window + a.sinks;
+        if (rows == 0) {
+            const int n = a.starts[b + 1] > a.starts[b] ? a.starts[b + 1] - a.starts[b] : 0;
+            rows = (n + tl.block_tokens - 1) / tl.block_tokens;
+        }
+        const float tiles = (float)(seen / KT + 1);
+        sum += (float)rows * tiles;
+        count += (float)rows;
+        most = fmaxf(most, tiles);
+    }
+    sum = wave_sum(sum);
+    count = wave_sum(count);
+    most = wave_max(most);
+    const float each = (float)(tl.head_tiles * a.kv_heads), slots = (float)tl.slots;  // blocks of a tile of rows
+    const float full = most * count < 1.05f * sum ? 1.0f : count * each < 0.6f * slots ? 0.85f : 1.7f;
+    const float share = sum * each / (full * slots);
+    return fmaxf(__uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(share))), (float)(tl.least / KT));
+}
+
 // DP: head_dim rounded up to 64, 96, 128 or 256. WAVES: of a block, 8 only in the form for many rows.
 template <typename E, bool Q8, int DP, bool KEYS, int WAVES, bool TREE>
 __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(ExtendArgs a, ExtendTiles tl) {
@@ -138,12 +168,19 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
     // ---- the block's rows
-    const uint32_t y = fast_div(blockIdx.x, tl.div_kv);
-    const int kvh = (int)(blockIdx.x - y * (uint32_t)a.kv_heads);
-    const uint32_t y2 = fast_div(y, tl.div_head_tiles);
-    const int ht = (int)(y - y2 * (uint32_t)tl.head_tiles);
-    // the last tiles of a stream see most and start first
-    int tile = tl.tiles - 1 - (int)y2;
+    uint32_t at_block = blockIdx.x;
+    auto digit = [&](const FastDiv &div, int of) {
+        const uint32_t rest = fast_div(at_block, div);
+        const int d = (int)(at_block - rest * (uint32_t)of);
+        at_block = rest;
+        return d;
+    };
+    const int kvh = digit(tl.div_kv, a.kv_heads);  // blocks of a kv head that follow each other go to one XCD's L2
+    const int ht = digit(tl.div_head_tiles, tl.head_tiles);
+    // the parts come last, so that the tiles that read the same tokens run together (the other way
+    // round: 347 us against 240 for the chunks of 512 tokens)
+    int tile = digit(tl.div_tiles, tl.tiles);
+    const int chunk = (int)at_block;
     int b, tok0, end;  // the stream, the tile's first token, the end of the stream's tokens
     if (tl.stream_tiles > 0) {
         b = (int)fast_div((uint32_t)tile, tl.div_stream_tiles);
@@ -173,7 +210,8 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
             if (past) {
                 const int l = __ffsll((unsigned long long)past) - 1;
                 b = b0 + l;
-                tok0 = __shfl(s0, l) + (tile - __shfl(sum - n, l)) * tl.block_tokens;
+                // the last tiles of a stream see most and start first
+                tok0 = __shfl(s0, l) + (__shfl(sum, l) - 1 - tile) * tl.block_tokens;
                 end = __shfl(s1, l);
                 break;
             }
@@ -212,19 +250,18 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
         if (base0 < sink_tiles * KT) base0 = sink_tiles * KT;
     }
     const int n_tiles = sink_tiles + (hi < base0 ? 0 : (hi - base0) / KT + 1);
-    const int chunk = blockIdx.y;
-    const int per_chunk = a.chunk_tokens / KT;
-    const int j0 = chunk * per_chunk;
-    const int j1 = n_tiles - j0 < per_chunk ? n_tiles : j0 + per_chunk;
+    // This block's part of them: as many equal parts as the rows' share of the card's work is worth.
+    int parts = 1;
+    if (a.chunks > 1) {
+        parts = (int)(n_tiles / part_tiles<KT>(a, tl, lane) + 0.4f);
+        parts = parts < 1 ? 1 : parts > a.chunks ? a.chunks : parts;
+        if (chunk >= parts) return;
+    }
+    const int per_part = (n_tiles + parts - 1) / parts;
+    const int j0 = chunk * per_part;
+    const int j1 = n_tiles - j0 < per_part ? n_tiles : j0 + per_part;
     const int64_t out_row = (int64_t)token * a.heads + head;
     const int64_t part = out_row * a.chunks + chunk;
-    if (j0 >= n_tiles && chunk > 0) {
-        if ((KEYS ? wave == 0 : true) && row < nrows && h == 0) {
-            a.part_ml[part * 2] = -INFINITY;
-            a.part_ml[part * 2 + 1] = 0.0f;
-        }
-        return;
-    }
     const int D = a.head_dim;
     auto tile_base = [&](int j) { return j < sink_tiles ? j * KT : base0 + (j - sink_tiles) * KT; };
     // The tiles that the rows of the tokens t0 .. t1 (of the block) all see whole: those before `first`,
@@ -775,7 +812,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
     // ---- results: the lane has dims 32 d + 8 g + 4 h + i of its row
     auto store_row = [&](float mm, float ll, auto value) {
         // value(d, g): 4 dims of the row
-        const bool whole = a.chunks == 1;
+        const bool whole = parts == 1;
         const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
         uint16_t *op = nullptr;
         if (whole) {
@@ -807,6 +844,8 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
             } else if (a.lse) {
                 a.lse[out_row] = (mm + log2f(ll)) * 0.69314718055994531f;
             }
+            // for the join: how many parts there are, none if the row is done
+            if (a.chunks > 1 && chunk == 0) a.part_count[out_row] = whole ? 0 : parts;
         }
     };
     l = half_sum(l);
@@ -846,7 +885,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
 }
 
 template <typename E, bool Q8, int DP, bool TREE> void run_form(const ExtendArgs &a, const ExtendTiles &t, hipStream_t s) {
-    const dim3 grid((unsigned)t.tiles * (unsigned)t.head_tiles * (unsigned)a.kv_heads, (unsigned)a.chunks);
+    const unsigned grid = (unsigned)t.tiles * (unsigned)t.head_tiles * (unsigned)a.kv_heads * (unsigned)a.chunks;
     if (t.form == ExtendForm::kKeys) extend_mfma<E, Q8, DP, true, 4, TREE><<<grid, 256, 0, s>>>(a, t);
     else if (t.form == ExtendForm::kRows128) extend_mfma<E, Q8, DP, false, 4, TREE><<<grid, 256, 0, s>>>(a, t);
     else if constexpr (DP <= 128) extend_mfma<E, Q8, DP, false, 8, TREE><<<grid, 512, 0, s>>>(a, t);

@@ -83,7 +83,8 @@ convt_status convt_cache_append(const convt_append_problem *problem, const void 
  * cache.kv_heads; the number of rows is below 2^24. q and out are
  * [tokens][heads][head_dim] with the given token and head strides. The
  * axis of t may be cut into parts that are computed by different blocks and
- * joined by a second kernel through the workspace.
+ * joined by a second kernel through the workspace (a close max_length saves
+ * room and blocks for parts that no stream reaches).
  * Routes: EXTEND_MFMA (two-byte types, head_dim a multiple of 16 and at most
  * 256, page_size a multiple of 16, 16-byte aligned rows of cache and q) on the
  * matrix cores, EXTEND_DIRECT for everything else, also at run time for
@@ -99,8 +100,8 @@ typedef enum convt_extend_route {
 typedef struct convt_extend_info {
     int64_t workspace_bytes;
     int32_t route;          /* the route chosen */
-    int32_t chunks;         /* parts the axis of t is cut into */
-    int32_t chunk_tokens;   /* tokens of a part */
+    int32_t chunks;         /* parts the axis of t is cut into, at most */
+    int32_t chunk_tokens;   /* tokens of a part of as many */
     int32_t reserved;
 } convt_extend_info;
 

@@ -147,7 +147,7 @@ def test_parts_cover_what_is_seen(length, batch, dim, dtype):
     for (st, i), sees, rows in asked:
         assert st == 0
         assert 1 <= i.chunks <= 32768 and i.chunks * i.chunk_tokens >= sees and i.chunk_tokens % 64 == 0
-        assert i.workspace_bytes == (0 if i.chunks == 1 else rows * 4 * i.chunks * (dim + 2) * 4)
+        assert i.workspace_bytes == (0 if i.chunks == 1 else rows * 4 * (i.chunks * (dim + 2) + 1) * 4)
 
 
 def test_python_refuses_host_tensors_and_wrong_names():
