@@ -19,7 +19,7 @@ namespace convt {
 
 namespace {
 
-constexpr int kRows = 4;  // rows a lane has in flight
+constexpr int kRows = 3;  // rows a lane has in flight
 
 // Cosine and sine of a by their Taylor polynomials on |x| <= pi / 4, where the
 // terms left out are below 2^-28; n counts quarter turns. An infinite or NaN
