@@ -188,7 +188,8 @@ __global__ __launch_bounds__(256) void extend_join(ExtendArgs a, int lanes_log2)
         real = real && (!a.starts || (token >= a.starts[0] && token < a.starts[a.batch]));
         out_at = token * a.out_stride[1];
     }
-    const int D = a.head_dim, n = real ? a.part_count[row] : 0;
+    // (rows that decreasing starts left to no block have any count)
+    const int D = a.head_dim, count = real ? a.part_count[row] : 0, n = count < a.chunks ? count : a.chunks;
     real = n > 0;
     const float *ml = a.part_ml + (int64_t)row * a.chunks * 2;
     float m = -INFINITY;

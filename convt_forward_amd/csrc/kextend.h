@@ -12,6 +12,12 @@ __device__ __forceinline__ int cut_length(const ExtendArgs &a, int b) {
     return len < 0 ? 0 : len > a.max_length ? a.max_length : len;
 }
 
+// starts[b] within the rows there are.
+__device__ __forceinline__ int cut_start(const ExtendArgs &a, int b) {
+    const int s = a.starts[b];
+    return s < 0 ? 0 : s > a.tokens ? a.tokens : s;
+}
+
 // The stream that row `token` of q belongs to and the end of its rows; -1 for
 // a row of no stream. starts does not decrease, so the first stream that ends
 // behind the row is found by halving; values that do decrease give some stream

@@ -120,8 +120,8 @@ template <int KT> __device__ __forceinline__ float part_tiles(const ExtendArgs &
         int seen = cut_length(a, b), rows = tl.stream_tiles;
         if (a.window > 0 && seen - a.sinks > a.window) seen = a.window + a.sinks;
         if (rows == 0) {
-            const int n = a.starts[b + 1] > a.starts[b] ? a.starts[b + 1] - a.starts[b] : 0;
-            rows = (n + tl.block_tokens - 1) / tl.block_tokens;
+            const int n = cut_start(a, b + 1) - cut_start(a, b);
+            rows = n > 0 ? (n + tl.block_tokens - 1) / tl.block_tokens : 0;
         }
         const float tiles = (float)(seen / KT + 1);
         sum += (float)rows * tiles;
@@ -195,11 +195,10 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
         for (int b0 = 0; b0 < a.batch; b0 += 64) {
             int s0 = 0, s1 = 0;
             if (b0 + lane < a.batch) {
-                s0 = a.starts[b0 + lane];
-                s1 = a.starts[b0 + lane + 1];
+                s0 = cut_start(a, b0 + lane);
+                s1 = cut_start(a, b0 + lane + 1);
             }
-            s0 = s0 < 0 ? 0 : s0 > a.tokens ? a.tokens : s0;
-            s1 = s1 < s0 ? s0 : s1 > a.tokens ? a.tokens : s1;
+            s1 = s1 < s0 ? s0 : s1;
             const int n = (s1 - s0 + tl.block_tokens - 1) / tl.block_tokens;
             int sum = n;
             for (int d = 1; d < 64; d *= 2) {

@@ -177,11 +177,12 @@ def _index(value):
     return None if value is None else operator.index(value)
 
 
-def _check_query(cache: KVCache, q, page_table, batch: int, out, axes: str) -> None:
+def _check_query(cache: KVCache, q, page_table, ragged: bool, out, axes: str) -> None:
+    """q and out have the axes; a page table has a row for each entry of q's first one, unless ragged."""
     if q.dim() != axes.count(",") + 1 or q.shape[-1] != cache.head_dim:
-        raise ValueError(f"q must be [{axes[:-4]}{cache.head_dim}]")
-    if page_table.dim() != 2 or page_table.shape[0] != batch:
-        raise ValueError(f"page_table must be [{batch}, pages]")
+        raise ValueError(f"q must be [{axes[:-3]}{cache.head_dim}]")
+    if page_table.dim() != 2 or not (ragged or page_table.shape[0] == q.shape[0]):
+        raise ValueError(f"page_table must be [{'batch' if ragged else q.shape[0]}, pages]")
     for t, name in ((q, "q"), (out, "out")):
         if t is not None and cache.head_dim > 1 and t.stride(-1) != 1:
             raise ValueError(f"the last axis of {name} must be contiguous")
@@ -222,10 +223,10 @@ def window_plan(cache: KVCache, q, page_table, ragged: bool = False, window: Opt
            out_stride, route)
 
     def make():
-        batch, width = page_table.shape if page_table.dim() == 2 else (0, 0)
         if window is not None and window < 1:
             raise ValueError("window must be at least 1 (None: everything before a token)")
-        _check_query(cache, q, page_table, batch if ragged else q.shape[0], out, "tokens, heads, dim")
+        _check_query(cache, q, page_table, ragged, out, "tokens, heads, dim")
+        batch, width = page_table.shape
         tokens, heads, dim = q.shape
         limit = 2 ** 62  # larger numbers mean no other thing
         return WindowProblem(cache._desc(q.dtype, "q"), width * cache.page_size if max_length is None else max_length, tokens,
@@ -306,7 +307,7 @@ def tree_plan(cache: KVCache, q, page_table, tree, scale=None, max_length: Optio
            out_stride, route)
 
     def make():
-        _check_query(cache, q, page_table, q.shape[0], out, "batch, drafts, heads, dim")
+        _check_query(cache, q, page_table, False, out, "batch, drafts, heads, dim")
         batch, drafts, heads, dim = q.shape
         words = (drafts + 63) // 64
         if tree.shape != (batch, drafts, words) and tree.shape != (drafts, words):
