@@ -63,7 +63,7 @@ struct ExtendTiles {
     int32_t tiles;          // of the grid
     int32_t slots;          // blocks that the card holds at once
     int32_t least;          // tokens that a part has at least
-    FastDiv div_kv, div_head_tiles, div_tiles, div_stream_tiles;
+    FastDiv div_kv, div_head_tiles, div_tiles, div_stream_tiles, div_block_tokens;
 };
 hipError_t launch_extend_bf16(const ExtendArgs &a, const ExtendTiles &t, hipStream_t stream);
 hipError_t launch_extend_f16(const ExtendArgs &a, const ExtendTiles &t, hipStream_t stream);

@@ -187,6 +187,7 @@ convt_status launch(const ExtendArgs &a, const convt_cache_desc &c, const convt_
         t.least = (int32_t)shape.least;
         t.div_kv = divisor_of((uint32_t)a.kv_heads);
         t.div_tiles = divisor_of((uint32_t)t.tiles);
+        t.div_block_tokens = divisor_of((uint32_t)t.block_tokens);
         t.div_head_tiles = divisor_of((uint32_t)t.head_tiles);
         t.div_stream_tiles = divisor_of((uint32_t)(t.stream_tiles > 0 ? t.stream_tiles : 1));
         if (c.quantised) e = c.dtype == CONVT_DTYPE_BF16 ? launch_extend_bf16_q8(a, t, s) : launch_extend_f16_q8(a, t, s);

@@ -182,24 +182,27 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
     int tile = digit(tl.div_tiles, tl.tiles);
     const int chunk = (int)at_block;
     int b, tok0, end;  // the stream, the tile's first token, the end of the stream's tokens
+    int len;           // the stream's cached tokens
     if (tl.stream_tiles > 0) {
         b = (int)fast_div((uint32_t)tile, tl.div_stream_tiles);
         const int in = tile - b * tl.stream_tiles;
         const int each = TREE ? a.drafts : 1;
         tok0 = b * each + in * tl.block_tokens;
         end = (b + 1) * each;
+        len = cut_length(a, b);
     } else {
         // 64 streams at a time: the tiles up to each of them
         b = -1;
-        tok0 = end = 0;
+        tok0 = end = len = 0;
         for (int b0 = 0; b0 < a.batch; b0 += 64) {
-            int s0 = 0, s1 = 0;
+            int s0 = 0, s1 = 0, ln = 0;
             if (b0 + lane < a.batch) {
                 s0 = cut_start(a, b0 + lane);
                 s1 = cut_start(a, b0 + lane + 1);
+                ln = cut_length(a, b0 + lane);
             }
             s1 = s1 < s0 ? s0 : s1;
-            const int n = (s1 - s0 + tl.block_tokens - 1) / tl.block_tokens;
+            const int n = (int)fast_div((uint32_t)(s1 - s0 + tl.block_tokens - 1), tl.div_block_tokens);
             int sum = n;
             for (int d = 1; d < 64; d *= 2) {
                 const int v = __shfl_up(sum, d);
@@ -212,6 +215,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                 // the last tiles of a stream see most and start first
                 tok0 = __shfl(s0, l) + (__shfl(sum, l) - 1 - tile) * tl.block_tokens;
                 end = __shfl(s1, l);
+                len = __shfl(ln, l);
                 break;
             }
             tile -= __shfl(sum, 63);
@@ -221,21 +225,24 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
     b = __builtin_amdgcn_readfirstlane(b);
     tok0 = __builtin_amdgcn_readfirstlane(tok0);
     end = __builtin_amdgcn_readfirstlane(end);
+    len = __builtin_amdgcn_readfirstlane(len);
     const int nt = end - tok0 < tl.block_tokens ? end - tok0 : tl.block_tokens;
     const int hs = a.share - ht * ROWS < ROWS ? a.share - ht * ROWS : ROWS;  // heads of the tile
     const int nrows = nt * hs;
     const int row = KEYS ? r32 : wave * 32 + r32;
     const int real_row = row < nrows ? row : nrows - 1;  // rows past the last compute as it does and are not stored
-    const int rt = real_row / hs;
+    // quotients of numbers up to 256: half a step off a whole one, the reciprocal's rounding does not matter
+    const float per_head = __builtin_amdgcn_rcpf((float)hs);
+    auto of_head = [&](int r) { return (int)(((float)r + 0.5f) * per_head); };
+    const int rt = of_head(real_row);
     const int token = tok0 + rt;
     const int head = kvh * a.share + ht * ROWS + real_row - rt * hs;
     // tokens of the wave's rows
     const bool idle = !KEYS && wave * 32 >= nrows;
     const int last = KEYS || wave * 32 + 31 >= nrows ? nrows - 1 : wave * 32 + 31;
-    const int rt0 = __builtin_amdgcn_readfirstlane(KEYS ? 0 : wave * 32 / hs), rt1 = __builtin_amdgcn_readfirstlane(last / hs);
+    const int rt0 = __builtin_amdgcn_readfirstlane(KEYS ? 0 : of_head(wave * 32)), rt1 = __builtin_amdgcn_readfirstlane(of_head(last));
 
     // ---- what they see
-    const int len = cut_length(a, b);
     const int pos0 = TREE ? 0 : len - (end - tok0);  // position of the tile's first token
     int hi, first_seen = 0, sink_tiles = 0, base0 = 0;  // the last token that any row sees; the first ones before the window
     if constexpr (TREE) {
