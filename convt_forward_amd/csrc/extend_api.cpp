@@ -43,11 +43,13 @@ Shape shape_of(ExtendForm form, int64_t batch, int64_t tokens, int64_t each, boo
     // ragged: every stream with rows may end in a tile of its own
     s.tiles = ragged ? tokens / s.block_tokens + (batch < tokens ? batch : tokens) : batch * s.stream_tiles;
     s.slots = 256 * (head_dim <= 128 && form != ExtendForm::kRows256 ? 2 : 1);
-    s.least = form == ExtendForm::kKeys ? 256 : 512;
+    s.least = form == ExtendForm::kKeys ? 128 : 512;
     return s;
 }
 // Rows of a stream that fit in 32 share their tokens among a block's waves; more go 128 or 256 to a block
-// (above 128 dims 128: a SIMD has the registers of one wave then, 4 a block). 256 rows a block are faster
+// (above 128 dims 128: a SIMD has the registers of one wave then, 4 a block). Measured, us, the form for few
+// rows and 128 rows, 4 heads sharing a kv head, 8 of these: trees of 8 drafts over 16 x 4096: 52, 52;
+// of 16: 59, 57; of 25 over ragged ones: 67, 51; one token in a window of 4096, 64 streams: 108, 160. 256 rows a block are faster
 // where blocks fill the card twice, or will do once the axis is cut, since it is long
 // against the new tokens; else the card's last blocks take too long. Measured, us, 128 and 256 rows, 32 / 8 heads of
 // 128, bf16: prompts of 512: 22, 27; 2048: 68, 66; 4096: 179, 155; 5 ragged chunks of 500 to 1000 in a
@@ -60,7 +62,9 @@ Shape pick_shape(int64_t batch, int64_t tokens, int64_t each, bool ragged, int64
         const int64_t blocks = s.tiles * s.head_tiles * kv_heads;
         if (blocks >= 2 * s.slots || (longest / 4 >= each && blocks * (longest / s.least) >= s.slots)) return s;
     }
-    return shape_of(ExtendForm::kRows128, batch, tokens, each, ragged, share, head_dim);
+    Shape s = shape_of(ExtendForm::kRows128, batch, tokens, each, ragged, share, head_dim);
+    if (longest / 4 >= each) s.least = 256;
+    return s;
 }
 
 // What window and tree problems are checked for alike, and the info of one
@@ -93,7 +97,11 @@ convt_status extend_check(const convt_cache_desc &c, int64_t max_length, int64_t
         // for the long ones. Blocks that fill the card twice need none. Measured, us (1, 2, 3, 4, 6, 8
         // parts): 16 ragged streams up to 4096, 25 drafts: 134, 80, 72, 62, 51, 64; 4 of 2100 to 8000, 512
         // new tokens: 277, 265, 227, 254, 257, 258; 64 in a window of 4096, one new token: 110, 117, 122, 126, 133, 141.
-        if (blocks == 0 || blocks >= 2 * shape->slots) chunks = 1;
+        // Up to 512 tokens one part: the join's launch takes as long (260 tokens: 8.8 us in one). Parts of few rows have
+        // 128 tokens at least, a step of each wave; of many 256, or 512 where the rows are most of the tokens.
+        // (1, 2, 4, 8, 16 parts) one token of 1024: 19.0, 16.7, 13.9, 12.9, -; of 4096: 54, 35, 23, 18, 16; 16
+        // drafts of 2048: 52, 33, 22, 18.5, 16.8; a prompt of 512: 22, 25, 26.
+        if (blocks == 0 || blocks >= 2 * shape->slots || longest <= 512) chunks = 1;
         else if (limited) chunks = shape->slots / blocks;
         else chunks = ceil_div((batch < 3 ? batch : 3) * shape->slots, blocks);
         least = shape->least;
@@ -258,6 +266,8 @@ convt_status convt_cache_append(const convt_append_problem *problem, const void 
     a.interleaved = p.interleaved;
     a.div_rows = divisor_of((uint32_t)per_token);
     a.div_half = divisor_of((uint32_t)(a.half > 0 ? a.half : 1));
+    // tokens of a block: many amortise the angles, few spread over the card. Measured, us, with 1, 2, 4, 8:
+    // 32767 tokens of 32 query heads: 203, 195, 178, 178. 64 tokens in blocks of 4 would leave 240 of 256 CUs idle.
     a.block_tokens = p.rows.tokens >= 4096 ? 4 : 1;
     return device_status(launch_append(a, c.dtype, c.quantised, (hipStream_t)stream));
 }
