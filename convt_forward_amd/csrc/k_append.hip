@@ -11,7 +11,9 @@
 // to within an eighth turn there; in float32 a position of 10^5 would leave it
 // 2^-8 off. Polynomials in float32 do the rest.
 // Memory traffic bounds it: q, k and v are read once, q_out and the cells written
-// once.
+// once. Measured: 32767 tokens, 32 + 8 heads of 128, bf16 to e4m3, 741 MB: 158 us back to back, 4.7 TB/s,
+// 95 % of a large copy's rate; 64 tokens 5.2 us, one 3.2 in a graph. Rows a lane has in flight
+// (2, 3, 4, 6): 177, 170, 178, 183 us.
 #include "extend.h"
 #include "kdecode.h"
 

@@ -21,7 +21,8 @@ constexpr int kWaves = 4;
 // with q (held in LDS), then the lanes turn to the head dimension and add the
 // 64 values p[t] V[t], one token after the other; a token that the row does not
 // see is not read. Simple and general: every row reads its keys again, so it
-// is far from the matrix-core kernel. It serves float32, odd head
+// is far from the matrix-core kernel (a prompt of 8192 in a window of 4096: 100 ms
+// against 0.44; one token of 64 streams: 1.9 ms against 0.10). It serves float32, odd head
 // dimensions, pages and alignments.
 template <typename T, bool Q8, bool TREE>
 __global__ __launch_bounds__(64 * kWaves) void extend_direct(ExtendArgs a) {
@@ -167,7 +168,8 @@ __global__ __launch_bounds__(64 * kWaves) void extend_direct(ExtendArgs a) {
 // Joins the parts of a row: out = sum 2^(m_c - m) O_c / sum 2^(m_c - m) l_c. A
 // part that saw nothing (m = -infinity, l = 0) has no O. 256 / ROWS threads a
 // row: 1 << lanes_log2 of them take 4 dims each, the others other parts.
-// ROWS = 1 where there are many parts, 4 where there are few.
+// ROWS = 1 where there are many parts, 4 where there are few. Reading the parts bounds it: 65536
+// rows of 128 dims, up to 3 parts: 21 us; 4096 rows, up to 18: 11 us.
 template <typename T, int ROWS>
 __global__ __launch_bounds__(256) void extend_join(ExtendArgs a, int lanes_log2) {
     constexpr int PER = 256 / ROWS;
