@@ -11,9 +11,10 @@
 // to within an eighth turn there; in float32 a position of 10^5 would leave it
 // 2^-8 off. Polynomials in float32 do the rest.
 // Memory traffic bounds it: q, k and v are read once, q_out and the cells written
-// once. Measured: 32767 tokens, 32 + 8 heads of 128, bf16 to e4m3, 741 MB: 158 us back to back, 4.7 TB/s,
-// 95 % of a large copy's rate; 64 tokens 5.2 us, one 3.2 in a graph. Rows a lane has in flight
-// (2, 3, 4, 6): 177, 170, 178, 183 us.
+// once. Measured: 32767 tokens, 32 + 8 heads of 128, bf16 to e4m3, 741 MB: 151 us back to back, 4.9 TB/s,
+// a large copy's rate; in a graph 158, 64 tokens 4.8 us, one 3.2. Rows a lane has in flight
+// (2, 3, 4, 6): 177, 170, 178, 183 us; waves of queries alone leave out the largest magnitude
+// and the scale: 160 us, 164 with them (before it). Offsets of 24-bit factors instead of 64: 8 % slower.
 #include "extend.h"
 #include "kdecode.h"
 
@@ -124,6 +125,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, int lanes_log
                     if (real && n > 0)
                         store8<T>((T *)a.q_out + (t0 + tok[u]) * a.q_stride[1][0] + head[u] * a.q_stride[1][1] + piece, f, n);
                 }
+                if (!__any(head[u] >= a.heads)) continue;  // the wave's rows are all queries
                 // the reduction is over all lanes, whatever their rows are
                 float s = 1.0f;
                 if constexpr (Q8) {
