@@ -274,3 +274,39 @@ def test_python_refusals():
             append(**kw)
     # a refused call leaves no plan behind that a right one would find
     append(q=q3)
+
+
+def test_nothing_to_do_and_nothing_to_see():
+    q = rand(3, 4, 64).bfloat16().to(DEV)
+    table, lengths = torch.zeros(3, 2, dtype=torch.int32, device=DEV), torch.full((3,), 20, dtype=torch.int32, device=DEV)
+    tree = C.tree_mask(torch.arange(-1, 2)).to(DEV)
+    # a cache without pages, and a page table without pages
+    for cache, t in ((C.KVCache.new(0, 2, 16, 64), table), (C.KVCache.new(4, 2, 16, 64), table[:, :0])):
+        for route in ("direct", "auto"):
+            out, lse = C.window_attention(q, cache, t, lengths, lse=True, route=route)
+            assert (out == 0).all() and (lse == -math.inf).all()
+            out, lse = C.tree_attention(q.view(3, 1, 4, 64).expand(3, 3, 4, 64), cache, t, lengths, tree, lse=True, route=route)
+            assert (out == 0).all() and (lse == -math.inf).all()
+    cache = C.KVCache.new(4, 2, 16, 64)
+    none = torch.zeros(1, dtype=torch.int32, device=DEV)
+    assert C.window_attention(q[:0], cache, table[:0], lengths[:0]).shape == (0, 4, 64)
+    assert C.window_attention(q[:0], cache, table[:0], lengths[:0], starts=none).shape == (0, 4, 64)
+    assert C.window_attention(q[:0], cache, table, lengths, starts=torch.zeros(4, dtype=torch.int32, device=DEV)).shape == (0, 4, 64)
+    assert C.tree_attention(q[:0].view(0, 1, 4, 64), cache, table[:0], lengths[:0], tree[:1]).shape == (0, 1, 4, 64)
+    out = torch.full_like(q, 5.0)
+    C.window_attention(q, cache, table[:0], lengths[:0], starts=none, out=out)  # rows of no stream
+    torch.cuda.synchronize()
+    assert (out == 5).all()
+
+
+def test_repeated_rows_of_what_is_read():
+    """A tree, a page table or queries given once for all streams, by strides of 0."""
+    s = Streams(3, 300, 1, 64, 16, "bf16", False, seed=76)
+    lengths = torch.tensor([200, 100, 280], dtype=torch.int32, device=DEV)
+    tree = C.tree_mask(random_tree(1, 12, 1)).to(DEV)
+    q = rand(1, 12, 4, 64, scale=2).bfloat16().to(DEV)
+    table = s.table.to(DEV)[:1]
+    for route in ("direct", "auto"):
+        a = C.tree_attention(q.expand(3, -1, -1, -1), s.cache, table.expand(3, -1), lengths, tree.expand(3, -1, -1), route=route)
+        b = C.tree_attention(q.repeat(3, 1, 1, 1), s.cache, table.repeat(3, 1), lengths, tree[0], route=route)
+        assert torch.equal(a, b)
