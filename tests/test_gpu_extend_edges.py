@@ -10,7 +10,7 @@ import torch
 import convt_forward_amd as C
 from tests.decode_util import TYPES, U, within
 from tests.extend_util import DEV, Streams, attend64, rand, row_bound, tree_seen, window_seen
-from tests.test_gpu_extend import check_tree, check_window, random_tree
+from tests.test_gpu_extend import check_tree, random_tree
 
 pytestmark = pytest.mark.gpu
 
