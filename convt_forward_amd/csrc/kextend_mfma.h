@@ -34,8 +34,11 @@
 //   their value. They carry a factor 2^7, so that those down to 2^-21 of
 //   the base keep their 11 bits and smaller ones are off by at most 2^-32
 //   of it. With e4m3 the logarithm of the value's scale is added to the score: the weight
-//   is p times the scale, in float16's range whatever the scales are, and
-//   the sum of p takes it off again.
+//   is p times the scale, in float16's range whatever the scales are. The sum of p is that of the
+//   weights times 1 / scale, which float32 holds for scales within 2^-40 .. 2^30. Values of smaller ones (rows of
+//   zeros have 2^-126) are left out of it; a pass over the tiles that hold them adds their p at the end,
+//   from the scores alone. Larger ones, or what is no number, make the sum NaN, and the pass forms it from all tiles.
+//   A weight below 2^-60 of the row's largest may be lost where waves or parts are joined.
 //   as the sum of two bfloat16 values (2^-16) in the form for few rows over
 //   bfloat16, where the second product costs nothing beside the loads, and as one
 //   (2^-8) in the forms for many, where it takes half as long again (a prompt of 8192
@@ -159,6 +162,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
     constexpr bool SPLIT = KEYS && __is_same(EV, __bf16);
     constexpr float RAISE = __is_same(EV, __bf16) ? 0.0f : 7.0f;  // the weights carry 2^RAISE
     constexpr uint32_t INF = __is_same(EV, __bf16) ? 0x7f80u : 0x7c00u, ONE = __is_same(EV, __bf16) ? 0x3f80u : 0x3c00u;
+    constexpr float SMALL = 0x1p-40f, LARGE = 0x1p30f;  // scales of e4m3 values that the sum of weights bears
     constexpr int KT = KEYS ? 32 : 64;           // tokens of a tile
     constexpr int NS = KT / 32, NG = KT / 16;
     constexpr int ROWS = KEYS ? 32 : 32 * WAVES; // of a block
@@ -172,7 +176,6 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
     constexpr int UNIT = KT * (KSTR + VSTR) + (Q8 ? 3 * KT * 4 : 0);
     constexpr int BUFFERS = WAVES == 8 ? 3 : 2;  // of tiles, in the form for many rows
     constexpr int NC = DP / 16, ND = DP / 32;
-    constexpr int AHEAD = WAVES == 8 ? 8 : 0;    // operands of V that are read before the products' phase
     __shared__ __attribute__((aligned(16))) char lds[(KEYS ? 4 : BUFFERS) * UNIT];
     __shared__ float m_lds[4][32], l_lds[4][32];
     __shared__ int there_lds[BUFFERS];  // whether a tile's groups have pages, a byte each
@@ -413,7 +416,9 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
         }
     };
     // Where some row of the block does not see some token of the tile in the registers (edge), values that no row
-    // sees become 0, infinities and NaN too unless `keep`. Returns whether there were any.
+    // sees become 0, infinities and NaN too unless `keep`. Returns whether there were any. In the form for few rows their
+    // scales become 1: most tiles at a stream's end would else bring the pass for scales far from 1 (the other forms, short of
+    // registers, meet them at the end of a prompt only).
     auto clean_tile = [&](int base, bool edge, bool keep) {
         bool bad = false;
         if (edge || there != (1u << GW) - 1) {
@@ -432,10 +437,13 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                             raw[s][g][i][k] = edge && !keep ? f : x;
                         }
                     }
+                if constexpr (Q8 && KEYS)
+                    if (base + 16 * g0 + lane > hi || !(there >> (lane / 16 % GW) & 1)) scale_raw[s] = 1.0f;
             }
         }
         return bad;
     };
+    uint32_t odd = 0;  // 1: a tile that not all rows see held infinities or NaN, 2: a value's scale was too small for the sum
     auto store_tile = [&](char *to) {
 #pragma unroll
         for (int s = 0; s < SIDES; ++s) {
@@ -473,10 +481,10 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                 if (lane < 16 * GW) {
                     float *sp = (float *)(to + KT * (KSTR + VSTR)) + 16 * g0 + lane;
                     if (is_v(s)) {
-                        // a scale that is not a number leaves the sum through its score alone
                         const float v = scale_raw[s] < 0x1p-126f ? 0x1p-126f : scale_raw[s];
+                        odd |= v < SMALL ? 2 : 0;
                         sp[KT] = log2f(v);
-                        sp[2 * KT] = v == v ? 1.0f / v : 0.0f;
+                        sp[2 * KT] = v < SMALL ? 0.0f : v <= LARGE ? 1.0f / v : __builtin_nanf("");
                     } else {
                         sp[0] = scale_raw[s] * c;
                     }
@@ -510,6 +518,18 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
             }
         }
     };
+    // The scores of what the row does not see become -infinity, by integers: as comparisons that two places of the kernel
+    // make, each would keep a pair of scalar registers.
+    auto mask = [&](int j, uint32_t ok) {
+        const uint64_t seen = seen_bits(tile_base(j), ok) >> (4 * h);
+#pragma unroll
+        for (int u = 0; u < NS; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t keep = (uint32_t)__builtin_amdgcn_sbfe((int)(uint32_t)(seen >> (32 * u)), 8 * (i / 4) + i % 4, 1);
+                s[u][i] = __uint_as_float((__float_as_uint(s[u][i]) & keep) | (0xff800000u & ~keep));
+            }
+    };
     auto weights = [&](const char *t, int j, uint32_t ok) {
         const float *sc = (const float *)(t + KT * (KSTR + VSTR)) + 4 * h;
         if constexpr (Q8) {
@@ -522,14 +542,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                     for (int i = 0; i < 4; ++i) s[u][g * 4 + i] = __builtin_fmaf(s[u][g * 4 + i], k[i], v[i]);
                 }
         }
-        if (ok != (1u << NG) - 1 || !whole.has(j)) {
-            const uint64_t seen = seen_bits(tile_base(j), ok) >> (4 * h);
-#pragma unroll
-            for (int u = 0; u < NS; ++u)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    s[u][i] = seen >> (32 * u + 8 * (i / 4) + i % 4) & 1 ? s[u][i] : -INFINITY;
-        }
+        if (ok != (1u << NG) - 1 || !whole.has(j)) mask(j, ok);
         float top = s[0][0];
 #pragma unroll
         for (int u = 0; u < NS; ++u)
@@ -582,19 +595,12 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
         const u32x2 x = read_transposed(p), y = read_transposed(p + 8 * VSTR);
         return u32x4{x[0], x[1], y[0], y[1]};
     };
-    u32x4 ahead[AHEAD > 0 ? AHEAD : 1];
-    auto read_ahead = [&](const char *t) {
-#pragma unroll
-        for (int f = 0; f < AHEAD; ++f) ahead[f] = v_word(t, f / ND, f % ND);
-    };
     auto values = [&](const char *t) {
 #pragma unroll
         for (int k = 0; k < NS * 2; ++k)
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                u32x4 w;
-                if (k * ND + d < AHEAD) w = ahead[k * ND + d];
-                else w = v_word(t, k, d);
+                u32x4 w = v_word(t, k, d);
                 o[d] = mfma32(__builtin_bit_cast(EV8, w), __builtin_bit_cast(EV8, ph[k]), o[d]);
                 if constexpr (SPLIT) {
                     // the low part may be 0 or negative: an infinite value takes part in the first product only
@@ -627,18 +633,40 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
         }
         __builtin_amdgcn_sched_group_barrier(PRODUCT, GV > 1 ? 8 : 4, 0);
     };
-    auto order_both = [&]() {  // values() of a tile whose first operands are there, then scores() of another
+    // The same with the order written out, where hints do not hold (they do until code elsewhere takes another register): an
+    // operand is read RING products ahead of its own, STEP at a time. The 8 waves' phase multiplies the values of a tile,
+    // whose first operands are there, and the scores of the next one; the 4 waves' two phases over e4m3 each do one
+    // of them. With a wait for each operand a prompt of 4096 over e4m3 takes 219 us, 201 so (200 to 204 with 4 to 12 ahead); 16
+    // trees of 25 drafts 61, 57 so (60 with 8 ahead, whose registers spill).
+    constexpr int RING = WAVES == 8 ? 8 : 4, STEP = RING / 2, NV = NS * 2 * ND, NP = NV + NS * NC;
+    u32x4 ring[RING];
+    auto operand = [&](const char *t, const char *next, int f) {
+        const int c = f - NV;
+        return f < NV ? v_word(t, f / ND, f % ND) : *(const u32x4 *)(next + k_at + c / NC * 32 * KSTR + c % NC * 32);
+    };
+    auto read_ahead = [&](const char *t, int from) {
 #pragma unroll
-        for (int i = 2; i < GV; ++i) {
-            __builtin_amdgcn_sched_group_barrier(READ, 8, 0);
-            __builtin_amdgcn_sched_group_barrier(PRODUCT, 4, 0);
-        }
+        for (int f = from; f < from + RING; ++f) ring[f % RING] = operand(t, t, f);
+    };
+    auto products = [&](const char *t, const char *next, int from, int to) {
+        if (to > NV)
 #pragma unroll
-        for (int i = 0; i < GK; ++i) {
-            __builtin_amdgcn_sched_group_barrier(READ, 4, 0);
-            __builtin_amdgcn_sched_group_barrier(PRODUCT, 4, 0);
+            for (int u = 0; u < NS; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
+#pragma unroll
+        for (int f0 = from; f0 < to; f0 += STEP) {
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int f = f0; f < f0 + STEP; ++f) {
+                const int c = f - NV;
+                if (f < NV) o[f % ND] = mfma32(__builtin_bit_cast(EV8, ring[f % RING]), __builtin_bit_cast(EV8, ph[f / ND]), o[f % ND]);
+                else s[c / NC] = mfma32(__builtin_bit_cast(E8, ring[f % RING]), q[c % NC], s[c / NC]);
+            }
+#pragma unroll
+            for (int f = f0 + RING; f < f0 + RING + STEP && f < to; ++f) ring[f % RING] = operand(t, next, f);
         }
-        __builtin_amdgcn_sched_group_barrier(PRODUCT, 8, 0);
+        __builtin_amdgcn_sched_barrier(0);
     };
     // Infinities and NaN of a tile that not all rows see: for each kind, whether the row sees one in the dim.
     auto add_kinds = [&](const char *t, int base) {
@@ -668,7 +696,69 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
         }
     };
 
-    bool bad = false;  // a tile that not all rows see held infinities or NaN
+    // The pass for scales that the sum of weights does not bear: l to a base of its own, a whole number, so that it
+    // moves by powers of two. `all`: from the beginning.
+    float ml = 0.0f;
+    auto move_sum = [&](float to) {
+        const float up = fmaxf(ml, floorf(to));
+        l *= up == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(ml - up);
+        ml = up;
+    };
+    auto begin_plain = [&](bool all) {
+        ml = all ? -INFINITY : m;
+        l = all ? 0.0f : l;
+        move_sum(all ? -INFINITY : m + 1.0f);
+    };
+    // whether the lane's token of tile j (after look_up) has a value of a small scale
+    auto has_low = [&](int j) {
+        const int g = lane / 16 % GW, t = tile_base(j) + 16 * g0 + lane;
+        int32_t page = entry[0];
+        int off = entry_off[0];
+        if (GW == 2 && g == 1) {
+            page = entry[GW - 1];
+            off = entry_off[GW - 1];
+        }
+        if (lane >= 16 * GW || t > hi || page < 0 || page >= a.n_pages) return false;
+        return a.v_scale[((int64_t)page * a.kv_heads + kvh) * a.page_size + off + lane % 16] < SMALL;
+    };
+    // adds the p of a tile's tokens, or of those with a small scale
+    auto add_plain = [&](const char *t, int j, uint32_t ok, bool all) {
+        scores(t);
+        const float *sc = (const float *)(t + KT * (KSTR + VSTR)) + 4 * h;
+#pragma unroll
+        for (int u = 0; u < NS; ++u)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const f32x4 k = *(const f32x4 *)(sc + u * 32 + g * 8), r = *(const f32x4 *)(sc + 2 * KT + u * 32 + g * 8);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[u][g * 4 + i] = all || r[i] == 0.0f ? s[u][g * 4 + i] * k[i] : -INFINITY;
+            }
+        mask(j, ok);
+        float top = s[0][0];
+#pragma unroll
+        for (int u = 0; u < NS; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
+        move_sum(half_max(top));
+        const float from = ml == -INFINITY ? 0.0f : ml;
+#pragma unroll
+        for (int u = 0; u < NS; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) l += __builtin_amdgcn_exp2f(s[u][i] - from);
+    };
+    // O to the base of l, and l to 0.5 .. 1: in two steps, as 2^(m - base) may pass float32's range
+    auto end_plain = [&]() {
+        const float both = half_sum(l);
+        const int e = __builtin_amdgcn_frexp_expf(both);
+        const float half = both == 0.0f ? 1.0f : __builtin_amdgcn_exp2f(0.5f * (m - ml - (float)e));
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[d][i] = o[d][i] * half * half;
+        m = both == 0.0f ? -INFINITY : ml + (float)e;
+        l = h == 0 ? __builtin_amdgcn_frexp_mantf(both) : 0.0f;
+    };
+
     if constexpr (KEYS) {
         // the tile is the wave's own: its stores are done before its reads, and those before the next stores
         auto own_order = [&]() {
@@ -683,7 +773,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
         }
         for (; j < j1; j += 4) {
             const uint32_t ok = there;
-            bad |= clean_tile(tile_base(j), !whole.has(j), false);
+            odd |= clean_tile(tile_base(j), !whole.has(j), false);
             store_tile(my_lds);
             own_order();
             load_tile();  // the wave's next one; past the end the last one, which is not used
@@ -695,7 +785,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
             order_values();
             own_order();
         }
-        if (__any(bad))
+        if (__any(odd & 1))
             for (j = j0 + wave; j < j1; j += 4) {
                 if (whole.has(j)) continue;
                 look_up(j);
@@ -706,11 +796,26 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                 add_kinds(my_lds, tile_base(j));
                 own_order();
             }
+        if constexpr (Q8)
+            if (__any((odd & 2) || l != l)) {
+                const bool all = __any(l != l);
+                begin_plain(all);
+                for (j = j0 + wave; j < j1; j += 4) {
+                    look_up(j);
+                    if (!all && !__any(has_low(j))) continue;
+                    load_tile();
+                    store_tile(my_lds);
+                    own_order();
+                    add_plain(my_lds, j, there, all);
+                    own_order();
+                }
+                end_plain();
+            }
     } else if (j0 < j1) {
         // Tile j, which is in the registers (past the end the last one again).
         auto clean = [&](int j, bool keep) {
             j = j < j1 ? j : j1 - 1;
-            bad |= clean_tile(tile_base(j), !block_whole.has(j), keep);
+            odd |= clean_tile(tile_base(j), !block_whole.has(j), keep);
         };
         auto store = [&](int buffer, bool flags) {
             store_tile(lds + buffer * UNIT);
@@ -748,8 +853,13 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
             for (int j = j0; j < j1; ++j, at ^= 1) {
                 const char *t = lds + at * UNIT;
                 if (!idle) {
-                    scores(t);
-                    order_scores();
+                    if constexpr (Q8) {
+                        read_ahead(t, NV);
+                        products(t, t, NV, NP);
+                    } else {
+                        scores(t);
+                        order_scores();
+                    }
                 }
                 // behind the products
                 clean(j + 1, false);
@@ -758,8 +868,13 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                 look_up(j + 3);
                 if (!idle) {
                     weights(t, j, ok_of(at));
-                    values(t);
-                    order_values();
+                    if constexpr (Q8) {
+                        read_ahead(t, 0);
+                        products(t, t, 0, NV);
+                    } else {
+                        values(t);
+                        order_values();
+                    }
                 }
                 __syncthreads();
             }
@@ -801,21 +916,19 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
 #pragma unroll
                     for (int k = 0; k < NS * 2; ++k) asm volatile("" : "+v"(ph[k]));
                     asm volatile("" : "+v"(l));
-                    read_ahead(t);
+                    read_ahead(t, 0);
                     clean(j + 2, false);
                     __syncthreads();
                     store(next(at, 2), flags);
                     load_tile();  // of j + 3
-                    values(t);
-                    scores(lds + next(at, 1) * UNIT);  // past the end of the last tile again, which is not used
-                    order_both();
+                    products(t, lds + next(at, 1) * UNIT, 0, NP);  // past the end of the last tile again, which is not used
                     __syncthreads();
                     at = next(at, 1);
                 }
             }
             if (!second) __syncthreads();
         }
-        if (__syncthreads_or(bad))
+        if (__syncthreads_or(odd & 1))
             for (int j = j0; j < j1; ++j) {
                 if (block_whole.has(j)) continue;
                 look_up(j);
@@ -825,6 +938,21 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                 __syncthreads();
                 if (!idle) add_kinds(lds, tile_base(j));
                 __syncthreads();
+            }
+        if constexpr (Q8)
+            if (__syncthreads_or((odd & 2) || l != l)) {
+                const bool all = __syncthreads_or(l != l);
+                begin_plain(all);
+                for (int j = j0; j < j1; ++j) {
+                    look_up(j);
+                    if (!all && !__syncthreads_or(has_low(j))) continue;
+                    load_tile();
+                    store(0, flags);
+                    __syncthreads();
+                    if (!idle) add_plain(lds, j, ok_of(0), all);
+                    __syncthreads();
+                }
+                end_plain();
             }
     }
 

@@ -74,9 +74,13 @@ convt_status convt_cache_append(const convt_append_problem *problem, const void 
  * -infinity. Tokens of a page id outside 0 .. n_pages - 1 are left out. What a
  * row does not see changes nothing, whatever it holds; an infinite or NaN value
  * that it sees makes its dim of the result so, a weight too small to be held
- * times an infinite value NaN.
+ * times an infinite value NaN. A weight below 2^-60 of the row's largest may
+ * be lost.
  * Scales of a quantised cache are positive, as its definition gives them
- * (smaller ones count as 2^-126).
+ * (smaller ones count as 2^-126). Those of values may differ by any factor: a
+ * row of zeros has its part in the sum of exponentials, and a scale that is not
+ * finite makes out NaN, not lse. (One outside 2^-40 .. 2^30 has the sum formed
+ * another way, for neighbours that do not see it too: its last bits may differ.)
  *
  * max_length bounds the tokens t < max_length that the call handles: at most
  * table_width * page_size and below 2^31 - 4096. heads is a multiple of
