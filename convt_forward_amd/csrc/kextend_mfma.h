@@ -25,8 +25,9 @@
 //           V 64 or 192: the reads then take all banks in turn.
 //
 // The running base of a row's exponents moves only when a score passes it by
-// 2^8 (the weights are at most 2^8 then): rescaling O for every new maximum
-// would cost as much as the exponentials.
+// 2^8: rescaling O for every new maximum would cost as much as the
+// exponentials. Weights over bfloat16 values carry 2^-8, so that none is above
+// 1 and their products with the largest values stay finite.
 //
 // Roundings: Q and K enter as stored (e4m3 codes are exact in bf16 and f16;
 // their scales multiply the float32 scores). Weights meet V
@@ -160,7 +161,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
     typedef typename Vec8<E>::type E8;
     typedef typename Vec8<EV>::type EV8;
     constexpr bool SPLIT = KEYS && __is_same(EV, __bf16);
-    constexpr float RAISE = __is_same(EV, __bf16) ? 0.0f : 7.0f;  // the weights carry 2^RAISE
+    constexpr float RAISE = __is_same(EV, __bf16) ? -8.0f : 7.0f;  // the weights carry 2^RAISE
     constexpr uint32_t INF = __is_same(EV, __bf16) ? 0x7f80u : 0x7c00u, ONE = __is_same(EV, __bf16) ? 0x3f80u : 0x3c00u;
     constexpr float SMALL = 0x1p-40f, LARGE = 0x1p30f;  // scales of e4m3 values that the sum of weights bears
     constexpr int KT = KEYS ? 32 : 64;           // tokens of a tile
