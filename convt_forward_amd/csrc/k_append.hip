@@ -25,13 +25,18 @@ namespace {
 constexpr int kRows = 3;  // rows a lane has in flight
 
 // Cosine and sine of a by their Taylor polynomials on |x| <= pi / 4, where the
-// terms left out are below 2^-28; n counts quarter turns. An infinite or NaN
-// angle gives NaN.
+// terms left out are below 2^-28; q counts quarter turns. Their number n is off
+// by 2^-53 of itself, so an angle beyond some 2^50 is brought there in several
+// steps (four for the largest there is). An infinite or NaN angle gives NaN.
 __device__ __forceinline__ void turn(double a, float &c, float &s) {
-    const double n = rint(a * 0.63661977236758134308);
-    double r = fma(n, -1.5707963267948965580, a);
-    r = fma(n, -6.1232339957367660359e-17, r);
-    const int q = (int)(n - 4.0 * floor(n * 0.25));
+    double r = a;
+    int q = 0;
+    do {
+        const double n = rint(r * 0.63661977236758134308);
+        r = fma(n, -1.5707963267948965580, r);
+        r = fma(n, -6.1232339957367660359e-17, r);
+        q += (int)(n - 4.0 * floor(n * 0.25));
+    } while (fabs(r) > 0.79);
     const float x = (float)r, z = x * x;
     const float sp = x + x * z * (-1.0f / 6 + z * (1.0f / 120 + z * (-1.0f / 5040 + z * (1.0f / 362880))));
     const float cp = 1.0f + z * (-0.5f + z * (1.0f / 24 + z * (-1.0f / 720 + z * (1.0f / 40320 + z * (-1.0f / 3628800)))));
