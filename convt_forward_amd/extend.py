@@ -96,7 +96,7 @@ def _append_problem(cache: KVCache, k, v, slots, positions, inv_freq, q, interle
         if q.dim() != 3 or q.shape[0] != tokens or q.shape[2] != dim:
             raise ValueError(f"q must be [{tokens}, heads, {dim}]")
         _check(q, "q", None, k.dtype, device)
-        heads = q.shape[1]
+        heads = _count(q.shape[1], "heads")
         if heads == 0:
             raise ValueError("q has no heads")
         if q_out is not None:
@@ -173,8 +173,18 @@ def _number(scale):
     return None if scale is None else float(scale)
 
 
+_LIMIT = 2 ** 62  # numbers beyond it mean no other thing than this; ctypes would cut them to 64 bits
+
+
 def _index(value):
-    return None if value is None else operator.index(value)
+    return None if value is None else max(-_LIMIT, min(operator.index(value), _LIMIT))
+
+
+def _count(value: int, name: str) -> int:
+    """A size that a problem holds in 32 bits, to which ctypes would cut it."""
+    if value >= 2 ** 31:
+        raise ValueError(f"more than 2^31 - 1 {name}")
+    return value
 
 
 def _check_query(cache: KVCache, q, page_table, ragged: bool, out, axes: str) -> None:
@@ -217,7 +227,7 @@ def window_plan(cache: KVCache, q, page_table, ragged: bool = False, window: Opt
                 max_length: Optional[int] = None, out=None, route: str = "auto") -> Tuple[WindowProblem, ExtendInfo]:
     """The problem and the route, parts and workspace size of a window_attention call on these
     tensors; ragged: whether starts is given."""
-    scale, max_length, window, sinks = _number(scale), _index(max_length), _index(window), operator.index(sinks)
+    scale, max_length, window, sinks = _number(scale), _index(max_length), _index(window), _index(operator.index(sinks))
     out_stride = None if out is None else out.stride()
     key = ("window", q.dtype, q.shape, q.stride(), page_table.shape, page_table.stride(), bool(ragged), window, sinks, scale, max_length,
            out_stride, route)
@@ -228,11 +238,10 @@ def window_plan(cache: KVCache, q, page_table, ragged: bool = False, window: Opt
         _check_query(cache, q, page_table, ragged, out, "tokens, heads, dim")
         batch, width = page_table.shape
         tokens, heads, dim = q.shape
-        limit = 2 ** 62  # larger numbers mean no other thing
         return WindowProblem(cache._desc(q.dtype, "q"), width * cache.page_size if max_length is None else max_length, tokens,
                              _strides(q.shape, q.stride()), _strides(q.shape, out_stride or (heads * dim, dim, 1)), width,
-                             page_table.stride(0) if batch > 1 else max(1, width), min(window or 0, limit),
-                             max(-1, min(sinks, limit)), batch, heads, 1 if ragged else 0, EXTEND_ROUTES[route],
+                             page_table.stride(0) if batch > 1 else max(1, width), window or 0, sinks,
+                             _count(batch, "streams"), _count(heads, "heads"), 1 if ragged else 0, EXTEND_ROUTES[route],
                              1.0 / math.sqrt(dim) if scale is None else scale, 0)
 
     return _plan(cache, key, make, "convt_window_query")
@@ -318,8 +327,8 @@ def tree_plan(cache: KVCache, q, page_table, tree, scale=None, max_length: Optio
         tree_stride = (_i64 * 2)(tree.stride(0) if tree.dim() == 3 and batch > 1 else 0, tree.stride(-2) if drafts > 1 else words)
         return TreeProblem(cache._desc(q.dtype, "q"), width * cache.page_size if max_length is None else max_length,
                            _strides(q.shape, q.stride()), _strides(q.shape, out_stride or (drafts * heads * dim, heads * dim, dim, 1)),
-                           tree_stride, width, page_table.stride(0) if batch > 1 else max(1, width), batch, drafts, heads,
-                           EXTEND_ROUTES[route], 1.0 / math.sqrt(dim) if scale is None else scale, 0)
+                           tree_stride, width, page_table.stride(0) if batch > 1 else max(1, width), _count(batch, "streams"),
+                           _count(drafts, "drafts"), _count(heads, "heads"), EXTEND_ROUTES[route], 1.0 / math.sqrt(dim) if scale is None else scale, 0)
 
     return _plan(cache, key, make, "convt_tree_query")
 
