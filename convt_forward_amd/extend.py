@@ -150,10 +150,12 @@ def cache_append(cache: KVCache, k, v, slots, positions, inv_freq, q=None, inter
 def tree_mask(parents):
     """The tree of tree_attention from its drafts' parents: int64 [..., drafts, (drafts + 63) // 64]
     whose bit j of row i says that draft j is i or one of its ancestors. parents [..., drafts]
-    holds for each draft the draft it follows, or -1 for one that follows the cached tokens; drafts
-    may come in any order. Plain torch, on parents' device."""
+    holds for each draft the draft it follows, or -1 (or any number that is no draft's) for one that
+    follows the cached tokens; drafts may come in any order. Plain torch, on parents' device."""
     drafts = parents.shape[-1]
     parents = parents.to(torch.int64)
+    # an index out of range would end the process where parents are on a device
+    parents = torch.where(parents < drafts, parents, -1)
     words = (drafts + 63) // 64
     at = torch.arange(drafts, device=parents.device)
     rows = torch.zeros(parents.shape + (words,), dtype=torch.int64, device=parents.device)
