@@ -383,7 +383,8 @@ def attend_plan(cache: KVCache, q, page_table, scale=None, max_length: Optional[
     if scale is not None:
         scale = float(scale)
     if max_length is not None:
-        max_length = operator.index(max_length)
+        # ctypes would cut it to 64 bits; numbers beyond 2^62 are refused as that is
+        max_length = max(-2 ** 62, min(operator.index(max_length), 2 ** 62))
     out_stride = None if out is None else out.stride()
     key = (q.dtype, q.shape, q.stride(), page_table.shape, page_table.stride(), scale, max_length, out_stride, route)
     got = cache._attends.get(key)

@@ -1,4 +1,4 @@
-"""GPU tests of calls of the operators of several new tokens that have to be refused: numbers that the
+"""GPU tests of calls of the attention and append operators that have to be refused: numbers that the
 C structs cannot hold."""
 import pytest
 import torch
@@ -18,6 +18,14 @@ def test_max_length_beyond_64_bits(max_length):
         C.window_attention(q, s.cache, table, lengths, max_length=max_length)
     with pytest.raises(C.ConvtError):
         C.tree_attention(q.view(2, 1, 4, 64), s.cache, table, lengths, tree, max_length=max_length)
+
+
+@pytest.mark.parametrize("max_length", [2 ** 64 + 100, 2 ** 64, 2 ** 63, -2 ** 64])
+def test_max_length_of_one_token_beyond_64_bits(max_length):
+    s = Streams(2, 200, 1, 64, 16, "bf16", False, seed=95)
+    q, lengths = rand(2, 4, 64).bfloat16().to(DEV), torch.tensor([150, 20], dtype=torch.int32, device=DEV)
+    with pytest.raises(C.ConvtError):
+        C.decode_attention(q, s.cache, s.table.to(DEV), lengths, max_length=max_length)
 
 
 def test_windows_and_sinks_beyond_64_bits_are_all_there_is():
