@@ -76,7 +76,8 @@ convt_status extend_check(const convt_cache_desc &c, int64_t max_length, int64_t
     const convt_status st = check_cache(c);
     if (st != CONVT_OK) return st;
     if (batch < 0 || tokens < 0 || heads < 1 || heads % c.kv_heads != 0) return CONVT_ERR_INVALID_ARGUMENT;
-    if (tokens > kMaxBlocks || tokens * heads > kMaxBlocks) return CONVT_ERR_UNSUPPORTED;
+    // (streams without rows take no blocks, but blocks go through all of them, with 32-bit indexes)
+    if (batch > kMaxBlocks || tokens > kMaxBlocks || tokens * heads > kMaxBlocks) return CONVT_ERR_UNSUPPORTED;
     if (table_width < 0 || table_width > kMaxIndex) return CONVT_ERR_INVALID_ARGUMENT;
     if (batch > 1 && !row_stride_ok(table_stride, table_width, true)) return CONVT_ERR_INVALID_ARGUMENT;
     if (max_length < 0 || max_length > kMaxIndex - 4096 || max_length > table_width * c.page_size)

@@ -84,7 +84,7 @@ convt_status convt_cache_append(const convt_append_problem *problem, const void 
  *
  * max_length bounds the tokens t < max_length that the call handles: at most
  * table_width * page_size and below 2^31 - 4096. heads is a multiple of
- * cache.kv_heads; the number of rows is below 2^24. q and out are
+ * cache.kv_heads; the numbers of rows and of streams are below 2^24. q and out are
  * [tokens][heads][head_dim] with the given token and head strides. The
  * axis of t may be cut into parts that are computed by different blocks and
  * joined by a second kernel through the workspace (a close max_length saves
