@@ -1,7 +1,7 @@
 // Attention of several new tokens per stream over the paged cache: the
 // direct kernel (any element type, head dimension, page size and alignment)
 // and the joining of the length axis's parts. The matrix-core kernel is in
-// k_extend_mfma.hip.
+// kextend_mfma.h, its instances in k_extend_{bf16,f16}{,_q8}.hip.
 //
 // The softmax runs on powers of two: with s = scale * log2(e) * <q, K[t]>,
 // p[t] = 2^(s - m) over the running maximum m, l = sum p, O = sum p V, and a
