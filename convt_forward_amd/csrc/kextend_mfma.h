@@ -417,9 +417,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
         }
     };
     // Where some row of the block does not see some token of the tile in the registers (edge), values that no row
-    // sees become 0, infinities and NaN too unless `keep`. Returns whether there were any. In the form for few rows their
-    // scales become 1: most tiles at a stream's end would else bring the pass for scales far from 1 (the other forms, short of
-    // registers, meet them at the end of a prompt only).
+    // sees become 0, infinities and NaN too unless `keep`. Returns whether there were any.
     auto clean_tile = [&](int base, bool edge, bool keep) {
         bool bad = false;
         if (edge || there != (1u << GW) - 1) {
@@ -438,14 +436,14 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                             raw[s][g][i][k] = edge && !keep ? f : x;
                         }
                     }
-                if constexpr (Q8 && KEYS)
-                    if (base + 16 * g0 + lane > hi || !(there >> (lane / 16 % GW) & 1)) scale_raw[s] = 1.0f;
             }
         }
         return bad;
     };
     uint32_t odd = 0;  // 1: a tile that not all rows see held infinities or NaN, 2: a value's scale was too small for the sum
-    auto store_tile = [&](char *to) {
+    // the tile at `base` to LDS; scales of values that no row sees are 1: what lies behind a stream would else bring
+    // the pass for scales far from it
+    auto store_tile = [&](char *to, int base) {
 #pragma unroll
         for (int s = 0; s < SIDES; ++s) {
             constexpr int PW = Q8 ? 2 : 1;  // 16-byte words of LDS for one of the cache
@@ -482,10 +480,12 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                 if (lane < 16 * GW) {
                     float *sp = (float *)(to + KT * (KSTR + VSTR)) + 16 * g0 + lane;
                     if (is_v(s)) {
-                        const float v = scale_raw[s] < 0x1p-126f ? 0x1p-126f : scale_raw[s];
+                        const bool seen = base + 16 * g0 + lane <= hi && (there >> (lane / 16 % GW) & 1);
+                        const float v = !seen ? 1.0f : scale_raw[s] < 0x1p-126f ? 0x1p-126f : scale_raw[s];
                         odd |= v < SMALL ? 2 : 0;
-                        sp[KT] = log2f(v);
-                        sp[2 * KT] = v < SMALL ? 0.0f : v <= LARGE ? 1.0f / v : __builtin_nanf("");
+                        // the instructions alone, a step off each: v is no denormal number
+                        sp[KT] = __builtin_amdgcn_logf(v);
+                        sp[2 * KT] = v < SMALL ? 0.0f : v <= LARGE ? __builtin_amdgcn_rcpf(v) : __builtin_nanf("");
                     } else {
                         sp[0] = scale_raw[s] * c;
                     }
@@ -775,7 +775,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
         for (; j < j1; j += 4) {
             const uint32_t ok = there;
             odd |= clean_tile(tile_base(j), !whole.has(j), false);
-            store_tile(my_lds);
+            store_tile(my_lds, tile_base(j));
             own_order();
             load_tile();  // the wave's next one; past the end the last one, which is not used
             look_up(j + 8);
@@ -792,7 +792,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                 look_up(j);
                 load_tile();
                 clean_tile(tile_base(j), true, true);
-                store_tile(my_lds);
+                store_tile(my_lds, tile_base(j));
                 own_order();
                 add_kinds(my_lds, tile_base(j));
                 own_order();
@@ -805,7 +805,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                     look_up(j);
                     if (!all && !__any(has_low(j))) continue;
                     load_tile();
-                    store_tile(my_lds);
+                    store_tile(my_lds, tile_base(j));
                     own_order();
                     add_plain(my_lds, j, there, all);
                     own_order();
@@ -818,8 +818,8 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
             j = j < j1 ? j : j1 - 1;
             odd |= clean_tile(tile_base(j), !block_whole.has(j), keep);
         };
-        auto store = [&](int buffer, bool flags) {
-            store_tile(lds + buffer * UNIT);
+        auto store = [&](int buffer, int j, bool flags) {
+            store_tile(lds + buffer * UNIT, tile_base(j < j1 ? j : j1 - 1));
             if (flags && lane == 0 && wave < 4) ((uint8_t *)&there_lds[buffer])[wave] = (uint8_t)there;
         };
         look_up(j0);
@@ -839,7 +839,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                 }
         }
         clean(j0, false);
-        store(0, true);
+        store(0, j0, true);
         load_tile();
         look_up(j0 + 2);
         const bool flags = __syncthreads_or(outside);
@@ -864,7 +864,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                 }
                 // behind the products
                 clean(j + 1, false);
-                store(at ^ 1, flags);
+                store(at ^ 1, j + 1, flags);
                 load_tile();
                 look_up(j + 3);
                 if (!idle) {
@@ -891,14 +891,14 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
             if (second) __syncthreads();
             if (idle) {
                 clean(j0 + 1, false);
-                store(1, flags);
+                store(1, j0 + 1, flags);
                 load_tile();
                 __syncthreads();
                 for (int j = j0; j < j1; ++j) {
                     look_up(j + 3);
                     clean(j + 2, false);
                     __syncthreads();
-                    store(next(at, 2), flags);
+                    store(next(at, 2), j + 2, flags);
                     load_tile();
                     __syncthreads();
                     at = next(at, 1);
@@ -906,7 +906,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
             } else {
                 scores(lds);
                 clean(j0 + 1, false);
-                store(1, flags);
+                store(1, j0 + 1, flags);
                 load_tile();
                 __syncthreads();
                 for (int j = j0; j < j1; ++j) {
@@ -920,7 +920,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                     read_ahead(t, 0);
                     clean(j + 2, false);
                     __syncthreads();
-                    store(next(at, 2), flags);
+                    store(next(at, 2), j + 2, flags);
                     load_tile();  // of j + 3
                     products(t, lds + next(at, 1) * UNIT, 0, NP);  // past the end of the last tile again, which is not used
                     __syncthreads();
@@ -935,7 +935,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                 look_up(j);
                 load_tile();
                 clean(j, true);
-                store(0, false);
+                store(0, j, false);
                 __syncthreads();
                 if (!idle) add_kinds(lds, tile_base(j));
                 __syncthreads();
@@ -948,7 +948,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                     look_up(j);
                     if (!all && !__syncthreads_or(has_low(j))) continue;
                     load_tile();
-                    store(0, flags);
+                    store(0, j, flags);
                     __syncthreads();
                     if (!idle) add_plain(lds, j, ok_of(0), all);
                     __syncthreads();

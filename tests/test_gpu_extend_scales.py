@@ -151,3 +151,29 @@ def test_value_scales_in_blocks_of_256_rows(kind, dt):
     run(kind, dt, "auto", Streams(4, 4700, 8, 64, 16, dt, True, seed=86), [4600, 3000, 0, 4636], [64] * 4, 32, None, 0, tree, chunks=True)
     new = 512 * 256 // (8 * 4) + 37
     run(kind, dt, "auto", Streams(1, new, 8, 64, 16, dt, True, seed=87), [new], [new], 32, 300, 1, chunks=False)
+
+
+@pytest.mark.parametrize("drafts,share,batch,kv,room", [(7, 4, 2, 1, 300), (25, 4, 2, 1, 300), (25, 4, 2, 1, 3000), (64, 4, 4, 8, 4700)])
+def test_what_lies_behind_a_stream_changes_no_bit(drafts, share, batch, kv, room):
+    """Codes and scales behind the last token that a stream's rows see: unwritten places, NaN, infinities, garbage."""
+    s = Streams(batch, room, kv, 64, 16, "bf16", True, seed=88)
+    lengths = [room - drafts - 37 * (b + 1) for b in range(batch)]
+    tree = C.tree_mask(random_tree(batch, drafts, 6))
+    q = rand(batch, drafts, kv * share, 64, seed=22, scale=2).bfloat16().to(DEV)
+    at = torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    starts = torch.tensor([drafts * b for b in range(batch + 1)], dtype=torch.int32, device=DEV)
+    first = None
+    for scale, code in ((1.0, 0x38), (0.0, 0), (math.nan, 0x7f), (math.inf, 0xff), (-3.0, 0x01), (1e38, 0x7e), (1e-42, 0x80)):
+        for b, n in enumerate(lengths):
+            t = torch.arange(n + drafts, s.room)
+            pages, offs = s.table[b, t // 16].long(), t % 16
+            for name in "kv":
+                s.host[name].view(torch.uint8)[pages, :, offs] = code
+                s.scale[name][pages, :, offs] = scale
+        for name in "kv":
+            getattr(s.cache, name).copy_(s.host[name].to(DEV))
+            getattr(s.cache, name + "_scale").copy_(s.scale[name].to(DEV))
+        got = C.tree_attention(q, s.cache, s.table.to(DEV), at, tree.to(DEV), lse=True)
+        got += C.window_attention(q.view(-1, kv * share, 64), s.cache, s.table.to(DEV), at + drafts, starts=starts, lse=True)
+        first = got if first is None else first
+        assert all(torch.equal(x, y) and x.isfinite().all() for x, y in zip(got, first)), scale
