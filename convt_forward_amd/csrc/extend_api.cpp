@@ -98,6 +98,9 @@ convt_status extend_check(const convt_cache_desc &c, int64_t max_length, int64_t
         // for the long ones. Blocks that fill the card twice need none. Measured, us (1, 2, 3, 4, 6, 8
         // parts): 16 ragged streams up to 4096, 25 drafts: 134, 80, 72, 62, 51, 64; 4 of 2100 to 8000, 512
         // new tokens: 277, 265, 227, 254, 257, 258; 64 in a window of 4096, one new token: 110, 117, 122, 126, 133, 141.
+        // At most as many, twice, three, four times as many as fill the card: the 16 streams: 66, 54, 54, 54; 6 chunks of 300 over
+        // 300 to 12000, e4m3: 306, 308, 276, 276; 8 of 256 over 256 to 16384, bf16: 416, 321, 323, 319; 32 trees of 8 over 1 to
+        // 8192, e4m3: 87, 73, 73, 73; but 8 of 64 over 1 to 8192, bf16: 76, 94, 95, 94, and of 16 over 1 to 16384: 81, 97, 98, 98.
         // Up to 512 tokens one part: the join's launch takes as long (260 tokens: 8.8 us in one). Parts of few rows have
         // 128 tokens at least, a step of each wave; of many 256, or 512 where the rows are most of the tokens.
         // (1, 2, 4, 8, 16 parts) one token of 1024: 19.0, 16.7, 13.9, 12.9, -; of 4096: 54, 35, 23, 18, 16; 16
@@ -267,8 +270,10 @@ convt_status convt_cache_append(const convt_append_problem *problem, const void 
     a.interleaved = p.interleaved;
     a.div_rows = divisor_of((uint32_t)per_token);
     a.div_half = divisor_of((uint32_t)(a.half > 0 ? a.half : 1));
-    // tokens of a block: many amortise the angles, few spread over the card. Measured, us, with 1, 2, 4, 8:
-    // 32767 tokens of 32 query heads: 203, 195, 178, 178. 64 tokens in blocks of 4 would leave 240 of 256 CUs idle.
+    // tokens of a block: many amortise the angles, few spread over the card. Measured, us, with 1, 2, 4, 8: 32 + 8 heads of 128,
+    // e4m3: 512 tokens: 6.3, 7.8, 11.8, 20.4; 1531: 11.8, 11.9, 15.4, 21.2; 3000: 19.3, 18.5, 18.9, 26.4; 4096: 24.0, 22.2, 22.8, 27.2;
+    // 16384: 93.5, 84.1, 83.0, 86.7. 8 + 2 heads of 64, bf16: 512: 3.9, 3.7, 4.2, 4.7; 3000: 9.9, 7.2, 5.6, 5.7; 4096: 12.2, 8.3,
+    // 6.5, 6.0; 16384: 40.8, 24.8, 17.0, 13.3 (few heads would take 4 from some 1000 tokens on).
     a.block_tokens = p.rows.tokens >= 4096 ? 4 : 1;
     return device_status(launch_append(a, c.dtype, c.quantised, (hipStream_t)stream));
 }

@@ -22,7 +22,7 @@ constexpr int kWaves = 4;
 // 64 values p[t] V[t], one token after the other; a token that the row does not
 // see is not read. Simple and general: every row reads its keys again, so it
 // is far from the matrix-core kernel (a prompt of 8192 in a window of 4096: 100 ms
-// against 0.44; one token of 64 streams: 1.9 ms against 0.10). It serves float32, odd head
+// against 0.45; one token of 64 streams: 1.9 ms against 0.10). It serves float32, odd head
 // dimensions, pages and alignments.
 template <typename T, bool Q8, bool TREE>
 __global__ __launch_bounds__(64 * kWaves) void extend_direct(ExtendArgs a) {
@@ -168,8 +168,10 @@ __global__ __launch_bounds__(64 * kWaves) void extend_direct(ExtendArgs a) {
 // Joins the parts of a row: out = sum 2^(m_c - m) O_c / sum 2^(m_c - m) l_c. A
 // part that saw nothing (m = -infinity, l = 0) has no O. 256 / ROWS threads a
 // row: 1 << lanes_log2 of them take 4 dims each, the others other parts.
-// ROWS = 1 where there are many parts, 4 where there are few. Reading the parts bounds it: 65536
-// rows of 128 dims, up to 3 parts: 21 us; 4096 rows, up to 18: 11 us.
+// ROWS = 1 where there are more than 16 parts, 4 where there are fewer. Reading the parts bounds it: 65536
+// rows of 128 dims, up to 3 parts: 21 us; 4096 rows, up to 18: 11 us. Attention and join, us, ROWS = 1 and 4: 32 rows of
+// up to 32 parts: 13.9, 16.0; 1024 of 52: 35, 42; 96 of 21: 22, 26; 192 of 21: 28.5, 30; 512 of 7: 17.9, 18.2; 1024 of 10: 21.5, 20.2;
+// 3200 of 16: 53.9, 52.7; 12800 of 11: 62.5, 53.0; 16384 of 12: 107, 95; but 16384 of 32: 178, 174.
 template <typename T, int ROWS>
 __global__ __launch_bounds__(256) void extend_join(ExtendArgs a, int lanes_log2) {
     constexpr int PER = 256 / ROWS;

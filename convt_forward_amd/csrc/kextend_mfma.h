@@ -43,7 +43,7 @@
 //   as the sum of two bfloat16 values (2^-16) in the form for few rows over
 //   bfloat16, where the second product costs nothing beside the loads, and as one
 //   (2^-8) in the forms for many, where it takes half as long again (a prompt of 8192
-//   tokens 657 us instead of 441, a large tree 461 instead of 323). Results then
+//   tokens 1.49 times as long, a large tree 1.43). Results then
 //   are as far off as one more rounding of theirs: 0.0022 of their norm, 0.0016 without.
 //
 // Tokens that only some rows of a tile see: their scores become -infinity by
@@ -53,13 +53,15 @@
 // rows that see them (inside the first one, its registers would have cost the
 // others' prefetch).
 //
-// Measured (kernel alone, 8 kv heads of 128, 4 query heads each): a prompt of 8192, window 4096, 16
-// sinks, bf16: 433 us, 950 TFLOP/s; a tile of 64 tokens takes a block 3700 cycles, 2048 of them
-// products of its two waves a SIMD. 64 drafts over 100 K and 131 K tokens, bf16: 300 us + 11 of the
-// join, 3.2 TB/s and 800 TFLOP/s; 4 chunks of 512 over 2100 to 8000, e4m3: 232 us with the join. 64
-// streams in a window of 4096, e4m3: 103 us, 5.0 TB/s. Tried and slower: 4 waves in the 8 waves'
-// order of phases (506 us the prompt, 470 so), wave priorities around the products (441
-// against 435), two tiles on their way in registers (490).
+// Measured (in a graph, 8 kv heads of 128, 4 query heads each): a prompt of 8192, window 4096, 16
+// sinks, bf16: 449 us, 920 TFLOP/s. 64 drafts over 100 K and 131 K tokens, bf16: 315 us, 11 of them the
+// join's, 3.1 TB/s and 800 TFLOP/s; 4 chunks of 512 over 2100 to 8000, e4m3: 249 us with the join. 64
+// streams in a window of 4096, e4m3: 107 us, 4.8 TB/s (100 back to back). The pass for value scales far from 1: rows of
+// zeros at the first token take 64 streams of 4096 from 117 to 130 us, a prompt of 4096 from 195 to 233; one
+// scale of 2^31 there to 160 and 350. Tried and slower: 4 waves in the 8 waves'
+// order of phases (1.08 times as long for the prompt), wave priorities around the products (1.01), two tiles on
+// their way in registers (1.13). For the pass: in the loop, behind the weights (chunks 281 us, 250 without it) or before them
+// (291), with a base of l's own in all tiles (278).
 #pragma once
 
 #include "extend.h"
@@ -128,9 +130,16 @@ constexpr int next_pow2(int n) { return n <= 1 ? 1 : 2 * next_pow2((n + 1) / 2);
 // holds (tl.slots), so that ragged streams, whose lengths only the device knows, give it as
 // many blocks as equal ones; tl.least at least. Unequal parts do not come out even on all
 // shader engines, and one block too many takes as long as all: they get 0.85 of the
-// card (trees of 25 drafts over 16 ragged streams: 56 us, 64 with all of it). Where the rows alone nearly fill it,
-// unequal streams are cut into smaller parts, so that the long ones end with the others
-// (4 chunks of 512 new tokens over 2100 to 8000: 235 us, uncut 293). All blocks form the same number.
+// card. Where the rows alone nearly fill it (0.6 of it), unequal streams are cut into smaller parts (1.7 times as many), so that the
+// long ones end with the others. All blocks form the same number. 8 / 32 kv heads of 128, us:
+//   0.6, 0.7, 0.85, 1 of the card: 16 trees of 25 drafts over 1 .. 4096 tokens, e4m3: 67, 60, 54, 68; 32 of 8 over
+//   1 .. 8192, e4m3: 89, 83, 74, 76; 5 of 40 over 500 .. 20000, 64 dims: 77, 74, 76, 87; but 8 of 16 over 1 .. 16384, bf16:
+//   83, 70, 98, 90, and 8 single tokens of 1 .. 32768, e4m3: 80, 69, 90, 85.
+//   1, 1.35, 1.7, 2.2 times as many: 4 chunks of 512 over 2100 .. 8000, e4m3: 255, 257, 252, 276; 6 of 300 over 300 .. 12000,
+//   e4m3: 310, 321, 275, 291; 8 of 256 over 256 .. 16384, bf16: 340, 328, 319, 318; but 16 of 128 over 128 .. 4096: 114, 120, 121, 121.
+//   The border of nearly full at 0, 0.3, 0.6, 0.9: the 16 trees: 65, 54, 53, 53; the 4 chunks: 252, 252, 252, 318.
+//   Unequal is a longest stream 1.05 times the mean: 4 equal trees of 64 over 16384: 103, taken as unequal 112; 16 trees
+//   of 25 taken as equal: 67.
 template <int KT> __device__ __forceinline__ float part_tiles(const ExtendArgs &a, const ExtendTiles &tl, int lane) {
     float sum = 0.0f, count = 0.0f, most = 0.0f;  // of the tiles that the last rows of each stream see, for each of its tiles of rows
     for (int b = lane; b < a.batch; b += 64) {

@@ -288,7 +288,9 @@ def window_attention(q, cache: KVCache, page_table, lengths, starts=None, window
     the table can hold). A given workspace is contiguous, with at least window_plan's
     workspace_bytes. Returns out [tokens, heads, head_dim]; with lse (True, or a float32 tensor
     [tokens, heads] to fill) the pair (out, lse). A row that sees nothing gets zeros and
-    -infinity. Rows behind the last stream's are not written."""
+    -infinity. Rows behind the last stream's are not written. On the matrix cores weights are rounded
+    to 11 bits over float16 and e4m3 caches, and over bfloat16 ones to 8, or 16 in calls of few rows
+    (convt_extend.h has the rule); route="direct" keeps float32."""
     _check(q, "q", None, None, cache.device)
     _check(page_table, "page_table", None, torch.int32, cache.device)
     if out is not None:

@@ -88,12 +88,20 @@ convt_status convt_cache_append(const convt_append_problem *problem, const void 
  * [tokens][heads][head_dim] with the given token and head strides. The
  * axis of t may be cut into parts that are computed by different blocks and
  * joined by a second kernel through the workspace (a close max_length saves
- * room and blocks for parts that no stream reaches).
+ * room and blocks for parts that no stream reaches). out and lse overlap no
+ * input.
  * Routes: EXTEND_MFMA (two-byte types, head_dim a multiple of 16 and at most
- * 256, page_size a multiple of 16, 16-byte aligned rows of cache and q) on the
+ * 256, page_size a multiple of 16, 16-byte aligned rows of cache and q, cache
+ * strides below 2^31 elements between pages and 2^25 between tokens) on the
  * matrix cores, EXTEND_DIRECT for everything else, also at run time for
  * pointers not so aligned. AUTO picks; a forced MFMA that cannot serve is
  * CONVT_ERR_UNSUPPORTED.
+ * EXTEND_DIRECT rounds the result alone. On the matrix cores a weight p is
+ * rounded where it meets its value: to float16 over float16 and quantised caches
+ * (2^-11 of it), over bfloat16 caches to the sum of two bfloat16 (2^-16) in calls of few
+ * rows a stream (new tokens times heads / kv_heads up to 32; ragged streams: on
+ * average), and to one (2^-8) in others, whose results are as far off as one
+ * more rounding of theirs makes them.
  */
 typedef enum convt_extend_route {
     CONVT_EXTEND_AUTO = 0,
