@@ -84,3 +84,27 @@ def test_append_turns_pairs_by_any_angle(interleaved):
     # sine and cosine are off by 2^-23 each, so the squares' sum of them by 2 sqrt(2) 2^-23; a dim's two products, its sum and
     # its rounding by 2^-24 each of |a| + |b| <= sqrt(2) times the length, which counts twice in the square
     within(lengths(got), want, want * (2 * 2 ** 0.5 * 2.0 ** -23 + 2 * 2 * 2 ** 0.5 * 4 * U), "length squared")
+
+
+@pytest.mark.parametrize("quantised", [False, True])
+@pytest.mark.parametrize("new,share", [(1, 4), (7, 2), (20, 4), (200, 2)])
+def test_the_longest_stream(new, share, quantised):
+    """A window at the end of 2^31 - 4097 tokens, and first tokens, is that of a short stream with the same pages there."""
+    longest = 2 ** 31 - 4097
+    s = Streams(1, 1024, 1, 64, 16, "bf16", quantised, seed=91)
+    width = longest // 16 + 1
+    table = torch.zeros(1, width, dtype=torch.int32, device=DEV)
+    near = s.table.to(DEV)
+    short = 40 * 16 + longest % 16
+    table[:, :2] = near[:, :2]
+    table[:, -40:] = near[:, 1:41]
+    q = rand(new, share, 64, seed=5, scale=2).bfloat16().to(DEV)
+    starts = torch.tensor([0, new], dtype=torch.int32, device=DEV)
+    for route in ("direct", "auto"):
+        for window, sinks in ((100, 0), (300, 3), (17, 20)):
+            a = C.window_attention(q, s.cache, table, torch.tensor([longest], dtype=torch.int32, device=DEV), starts=starts, window=window, sinks=sinks,
+                                   max_length=longest, lse=True, route=route)
+            b = C.window_attention(q, s.cache, near, torch.tensor([short], dtype=torch.int32, device=DEV), starts=starts, window=window, sinks=sinks,
+                                   lse=True, route=route)
+            # the window begins as far into a page in both, so the same tokens share tiles
+            assert all(torch.equal(x, y) for x, y in zip(a, b)), (route, window, sinks)
