@@ -11,8 +11,8 @@
 // to within an eighth turn there; in float32 a position of 10^5 would leave it
 // 2^-8 off. Polynomials in float32 do the rest.
 // Memory traffic bounds it: q, k and v are read once, q_out and the cells written
-// once. Measured: 32767 tokens, 32 + 8 heads of 128, bf16 to e4m3, 741 MB: 153 us back to back, 4.9 TB/s,
-// a large copy's rate; in a graph 160, 64 tokens 4.9 us, one 3.3. Rows a lane has in flight
+// once. Measured: 32767 tokens, 32 + 8 heads of 128, bf16 to e4m3, 741 MB: 155 us back to back, 4.8 TB/s,
+// a large copy's rate; in a graph 163, 64 tokens 4.9 us, one 3.3. Rows a lane has in flight
 // (2, 3, 4, 6): 177, 170, 178, 183 us; waves of queries alone leave out the largest magnitude
 // and the scale: 160 us, 164 with them (before it). Offsets of 24-bit factors instead of 64: 8 % slower.
 #include "extend.h"

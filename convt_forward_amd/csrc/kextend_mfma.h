@@ -54,11 +54,11 @@
 // others' prefetch).
 //
 // Measured (in a graph, 8 kv heads of 128, 4 query heads each): a prompt of 8192, window 4096, 16
-// sinks, bf16: 449 us, 920 TFLOP/s. 64 drafts over 100 K and 131 K tokens, bf16: 315 us, 11 of them the
-// join's, 3.1 TB/s and 800 TFLOP/s; 4 chunks of 512 over 2100 to 8000, e4m3: 249 us with the join. 64
-// streams in a window of 4096, e4m3: 107 us, 4.8 TB/s (100 back to back). The pass for value scales far from 1: rows of
-// zeros at the first token take 64 streams of 4096 from 117 to 130 us, a prompt of 4096 from 195 to 233; one
-// scale of 2^31 there to 160 and 350. Tried and slower: 4 waves in the 8 waves'
+// sinks, bf16: 449 us, 920 TFLOP/s. 64 drafts over 100 K and 131 K tokens, bf16: 343 us, 11 of them the
+// join's, 2.9 TB/s and 730 TFLOP/s (327 back to back); 4 chunks of 512 over 2100 to 8000, e4m3: 233 us with the join. 64
+// streams in a window of 4096, e4m3: 109 us, 4.7 TB/s (102 back to back). The pass for value scales far from 1: rows of
+// zeros at the first token take 64 streams of 4096 from 118 to 130 us, a prompt of 4096 from 191 to 225; one
+// scale of 2^31 there to 161 and 339. Tried and slower: 4 waves in the 8 waves'
 // order of phases (1.08 times as long for the prompt), wave priorities around the products (1.01), two tiles on
 // their way in registers (1.13). For the pass: in the loop, behind the weights (chunks 281 us, 250 without it) or before them
 // (291), with a base of l's own in all tiles (278).
@@ -646,8 +646,10 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
     // The same with the order written out, where hints do not hold (they do until code elsewhere takes another register): an
     // operand is read RING products ahead of its own, STEP at a time. The 8 waves' phase multiplies the values of a tile,
     // whose first operands are there, and the scores of the next one; the 4 waves' two phases over e4m3 each do one
-    // of them. With a wait for each operand a prompt of 4096 over e4m3 takes 219 us, 201 so (200 to 204 with 4 to 12 ahead); 16
-    // trees of 25 drafts 61, 57 so (60 with 8 ahead, whose registers spill).
+    // of them. With a wait for each operand a prompt of 4096 over e4m3 takes 219 us, 190 so (as with 4 to 12 ahead; 203 where nothing
+    // else may move between them, though a long tree over bf16 takes 328 then, 343 so); 16 trees of 25 drafts 61, 57 so
+    // (60 with 8 ahead, whose registers spill).
+    constexpr int PASS = 0x2 | 0x4 | 0x20;  // what may move between them: other arithmetic, global loads
     constexpr int RING = WAVES == 8 ? 8 : 4, STEP = RING / 2, NV = NS * 2 * ND, NP = NV + NS * NC;
     u32x4 ring[RING];
     auto operand = [&](const char *t, const char *next, int f) {
@@ -666,7 +668,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
                 for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
 #pragma unroll
         for (int f0 = from; f0 < to; f0 += STEP) {
-            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_sched_barrier(PASS);
 #pragma unroll
             for (int f = f0; f < f0 + STEP; ++f) {
                 const int c = f - NV;
@@ -676,7 +678,7 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void extend_mfma(Ext
 #pragma unroll
             for (int f = f0 + RING; f < f0 + RING + STEP && f < to; ++f) ring[f % RING] = operand(t, next, f);
         }
-        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_sched_barrier(PASS);
     };
     // Infinities and NaN of a tile that not all rows see: for each kind, whether the row sees one in the dim.
     auto add_kinds = [&](const char *t, int base) {
